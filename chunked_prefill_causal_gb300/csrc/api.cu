@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "fp8.cuh"
+#include "serve.cuh"
 #include "vpp.h"
 
 namespace vpp {
@@ -1142,6 +1143,170 @@ int vpp_topk_chunk_attn_fp8(const void* q, const void* k_cache, const void* v_ca
 size_t vpp_topk_chunk_attn_workspace_size(int64_t chunk_len, int32_t topk, int heads, int head_dim) {
   if (chunk_len <= 0 || topk < 1 || heads <= 0 || head_dim <= 0) return 0;
   return topk_ws_bytes(chunk_len, topk, heads, head_dim);
+}
+
+// ------------------------------------------------------------- device-planned serving step
+namespace {
+
+// Any whole group of 1 to 16 query heads per kv head.
+int check_groups(int heads, int kv_heads) {
+  if (heads <= 0 || kv_heads <= 0 || heads % kv_heads != 0) return VPP_ERR_INVALID;
+  return heads / kv_heads <= 16 ? VPP_OK : VPP_ERR_UNSUPPORTED;
+}
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A [tokens][row] operand: 16-byte aligned rows that do not overlap.
+bool strided_ok(const void* p, int64_t stride, int64_t row) {
+  return p && aligned16(p) && stride >= row && stride % 8 == 0 && stride <= INT32_MAX;
+}
+
+constexpr int64_t kMaxPackedRows = INT32_MAX / 2;
+
+int rope_append_impl(bool fp8, RopeParams p, int interleaved, cudaStream_t st) {
+  if (p.total_q < 0 || p.total_q > kMaxPackedRows || p.batch < 0) return VPP_ERR_INVALID;
+  if (p.total_q == 0) return VPP_OK;  // pointers may be NULL without rows
+  if (p.batch == 0 || !p.cu || !aligned4(p.cu) || !aligned4(p.ctx)) return VPP_ERR_INVALID;
+  if (p.kv_heads <= 0 || p.kv_heads > 1024 || (p.q && (p.heads <= 0 || p.heads > 16384))) return VPP_ERR_INVALID;
+  if (p.dq <= 0 || p.dv <= 0 || p.dq % 64 || p.dv % 64 || p.dq > 512 || p.dv > 512) return VPP_ERR_UNSUPPORTED;
+  if (p.rot_dim < 0 || p.rot_start < 0 || p.rot_start > p.dq - p.rot_dim) return VPP_ERR_INVALID;
+  if (p.rot_dim % 16 || p.rot_start % 8) return VPP_ERR_UNSUPPORTED;
+  if (p.rot_dim > 0 && (!p.cos_sin || !aligned16(p.cos_sin) || p.table_rows <= 0)) return VPP_ERR_INVALID;
+  const int64_t q_row = (int64_t)p.heads * p.dq, k_row = (int64_t)p.kv_heads * p.dq;
+  if (p.q ? !strided_ok(p.q, p.q_stride, q_row) || !strided_ok(p.q_out, p.q_out_stride, q_row) : p.q_out != nullptr)
+    return VPP_ERR_INVALID;
+  if (!strided_ok(p.k, p.k_stride, k_row) || (p.k_out && !strided_ok(p.k_out, p.k_out_stride, k_row)))
+    return VPP_ERR_INVALID;
+  if ((p.q && p.q_out == p.q && p.q_out_stride != p.q_stride) || (p.k_out == p.k && p.k_out_stride != p.k_stride))
+    return VPP_ERR_INVALID;
+  if (p.k_cache || p.v_cache) {
+    if (!p.k_cache || !p.v_cache || !aligned16(p.k_cache) || !aligned16(p.v_cache)) return VPP_ERR_INVALID;
+    if (!strided_ok(p.v, p.v_stride, (int64_t)p.kv_heads * p.dv)) return VPP_ERR_INVALID;
+    if (!p.block_table || !aligned4(p.block_table) || p.max_blocks_per_seq <= 0 || p.num_blocks <= 0)
+      return VPP_ERR_INVALID;
+  } else if (fp8 || !p.k_out) {
+    return VPP_ERR_INVALID;
+  }
+  if (fp8 && !scales_ok(p.k_scale, p.v_scale)) return VPP_ERR_INVALID;
+  DeviceState* ds = nullptr;
+  if (int r = device_state(&ds)) return r;
+  p.status = ds->status;
+  return launch_rope_append(p, interleaved != 0, fp8, ds->num_sms, st) == cudaSuccess ? VPP_OK : VPP_ERR_CUDA;
+}
+
+int decode_attn_impl(bool fp8, PagedDecodeParams p, float softmax_scale, void* workspace, size_t workspace_bytes,
+                     cudaStream_t st) {
+  if (p.batch < 0) return VPP_ERR_INVALID;
+  if (p.batch == 0) return VPP_OK;  // pointers may be NULL without rows
+  if (int r = check_groups(p.heads, p.kv_heads)) return r;
+  if (!supported_dims(p.dq, p.dv) || p.kv_heads > 1024) return VPP_ERR_UNSUPPORTED;
+  if (!strided_ok(p.q, p.q_stride, (int64_t)p.heads * p.dq)) return VPP_ERR_INVALID;
+  if (!p.k_cache || !p.v_cache || !p.block_table || !p.ctx || !p.out) return VPP_ERR_INVALID;
+  if (!aligned16(p.k_cache) || !aligned16(p.v_cache) || !aligned16(p.out) || !aligned4(p.block_table) ||
+      !aligned4(p.ctx) || !aligned4(p.lse))
+    return VPP_ERR_INVALID;
+  if (p.max_blocks_per_seq <= 0 || p.num_blocks <= 0) return VPP_ERR_INVALID;
+  if ((int64_t)p.max_blocks_per_seq * kBlockTokens > INT32_MAX) return VPP_ERR_INVALID;
+  if (fp8 && !scales_ok(p.k_scale, p.v_scale)) return VPP_ERR_INVALID;
+  DeviceState* ds = nullptr;
+  if (int r = device_state(&ds)) return r;
+  const size_t need = paged_decode_ws_bytes(p.batch, p.heads, p.kv_heads, p.dq, p.dv, ds->num_sms);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return VPP_ERR_WORKSPACE;
+  p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p.dq)) * 1.4426950408889634f;
+  p.status = ds->status;
+  return launch_paged_decode(p, fp8, workspace, ds->num_sms, st) == cudaSuccess ? VPP_OK : VPP_ERR_CUDA;
+}
+
+}  // namespace
+
+int vpp_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const float* cos_sin, int32_t table_rows, int rot_start, int rot_dim,
+                    int interleaved, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                    void* k_cache, void* v_cache, const int32_t* block_table, int32_t max_blocks_per_seq,
+                    int32_t num_blocks, const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t batch,
+                    int64_t total_q, int heads, int kv_heads, int head_dim_qk, int head_dim_v, void* stream) {
+  const RopeParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                     static_cast<const uint16_t*>(v), static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out),
+                     k_cache, v_cache, nullptr, nullptr, cos_sin, block_table, cu_seqlens_q, ctx_lens,
+                     q_stride, k_stride, v_stride, q_out_stride, k_out_stride, total_q, batch, max_blocks_per_seq,
+                     num_blocks, table_rows, heads, kv_heads, head_dim_qk, head_dim_v, rot_start, rot_dim, nullptr};
+  return rope_append_impl(false, p, interleaved, as_stream(stream));
+}
+
+int vpp_rope_append_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                        int64_t v_stride, const float* cos_sin, int32_t table_rows, int rot_start, int rot_dim,
+                        int interleaved, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                        void* k_cache, void* v_cache, const float* k_scale, const float* v_scale,
+                        const int32_t* block_table, int32_t max_blocks_per_seq, int32_t num_blocks,
+                        const int32_t* cu_seqlens_q, const int32_t* ctx_lens, int32_t batch, int64_t total_q,
+                        int heads, int kv_heads, int head_dim_qk, int head_dim_v, void* stream) {
+  const RopeParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                     static_cast<const uint16_t*>(v), static_cast<uint16_t*>(q_out), static_cast<uint16_t*>(k_out),
+                     k_cache, v_cache, k_scale, v_scale, cos_sin, block_table, cu_seqlens_q, ctx_lens,
+                     q_stride, k_stride, v_stride, q_out_stride, k_out_stride, total_q, batch, max_blocks_per_seq,
+                     num_blocks, table_rows, heads, kv_heads, head_dim_qk, head_dim_v, rot_start, rot_dim, nullptr};
+  return rope_append_impl(true, p, interleaved, as_stream(stream));
+}
+
+int vpp_decode_attn(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                    const int32_t* block_table, int32_t max_blocks_per_seq, int32_t num_blocks,
+                    const int32_t* ctx_lens, int32_t batch, int heads, int kv_heads, int head_dim_qk,
+                    int head_dim_v, float softmax_scale, void* out, float* lse, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const PagedDecodeParams p{static_cast<const uint16_t*>(q), k_cache, v_cache, nullptr, nullptr, block_table,
+                            ctx_lens, static_cast<uint16_t*>(out), lse, q_stride, batch, max_blocks_per_seq,
+                            num_blocks, heads, kv_heads, head_dim_qk, head_dim_v, 0.f, nullptr};
+  return decode_attn_impl(false, p, softmax_scale, workspace, workspace_bytes, as_stream(stream));
+}
+
+int vpp_decode_attn_fp8(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, const int32_t* block_table,
+                        int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t* ctx_lens, int32_t batch,
+                        int heads, int kv_heads, int head_dim_qk, int head_dim_v, float softmax_scale, void* out,
+                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  const PagedDecodeParams p{static_cast<const uint16_t*>(q), k_cache, v_cache, k_scale, v_scale, block_table,
+                            ctx_lens, static_cast<uint16_t*>(out), lse, q_stride, batch, max_blocks_per_seq,
+                            num_blocks, heads, kv_heads, head_dim_qk, head_dim_v, 0.f, nullptr};
+  return decode_attn_impl(true, p, softmax_scale, workspace, workspace_bytes, as_stream(stream));
+}
+
+size_t vpp_decode_attn_workspace_size(int32_t batch, int heads, int kv_heads, int head_dim_qk, int head_dim_v) {
+  if (batch <= 0 || check_groups(heads, kv_heads) || !supported_dims(head_dim_qk, head_dim_v) || kv_heads > 1024)
+    return 0;
+  DeviceState* ds = nullptr;
+  const int num_sms = device_state(&ds) == VPP_OK ? ds->num_sms : 152;
+  return paged_decode_ws_bytes(batch, heads, kv_heads, head_dim_qk, head_dim_v, num_sms);
+}
+
+int vpp_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, const int32_t* cu_seqlens, int32_t batch, int64_t total_q, int heads,
+                    int kv_heads, int head_dim_qk, int head_dim_v, float softmax_scale, void* out, float* lse,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (total_q < 0 || total_q > kMaxPackedRows || batch < 0) return VPP_ERR_INVALID;
+  if (total_q == 0) return VPP_OK;  // pointers may be NULL without rows
+  if (batch == 0 || !cu_seqlens || !aligned4(cu_seqlens)) return VPP_ERR_INVALID;
+  if (int r = check_groups(heads, kv_heads)) return r;
+  if (!supported_dims(head_dim_qk, head_dim_v) || kv_heads > 1024) return VPP_ERR_UNSUPPORTED;
+  if (!strided_ok(q, q_stride, (int64_t)heads * head_dim_qk) ||
+      !strided_ok(k, k_stride, (int64_t)kv_heads * head_dim_qk) ||
+      !strided_ok(v, v_stride, (int64_t)kv_heads * head_dim_v))
+    return VPP_ERR_INVALID;
+  if (!out || !aligned16(out) || !aligned4(lse)) return VPP_ERR_INVALID;
+  DeviceState* ds = nullptr;
+  if (int r = device_state(&ds)) return r;
+  const size_t need = prompt_ws_bytes(batch, total_q, heads, kv_heads);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return VPP_ERR_WORKSPACE;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)head_dim_qk);
+  const PromptParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
+                       static_cast<const uint16_t*>(v), cu_seqlens, static_cast<uint16_t*>(out), lse,
+                       q_stride, k_stride, v_stride, total_q, batch, heads, kv_heads, head_dim_qk, head_dim_v,
+                       scale * 1.4426950408889634f, ds->status};
+  return launch_prompt_attn(p, workspace, ds->num_sms, as_stream(stream)) == cudaSuccess ? VPP_OK : VPP_ERR_CUDA;
+}
+
+size_t vpp_prompt_attn_workspace_size(int32_t batch, int64_t total_q, int heads, int kv_heads) {
+  if (batch <= 0 || total_q <= 0 || total_q > kMaxPackedRows || check_groups(heads, kv_heads)) return 0;
+  return prompt_ws_bytes(batch, total_q, heads, kv_heads);
 }
 
 int vpp_last_device_status(void* stream, int* code) {

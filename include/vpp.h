@@ -413,6 +413,158 @@ size_t vpp_topk_chunk_attn_workspace_size(int64_t chunk_len, int32_t topk,
                                           int heads, int head_dim);
 
 /*
+ * Serving-step operators with the lengths on the DEVICE.  They read
+ * cu_seqlens and ctx_lens when they run, not when they are called, so a CUDA
+ * graph that captured them serves every later step: update the arrays in
+ * place and replay.  Launch shapes depend on the host arguments alone.
+ * Lengths and block-table entries are checked on the device: what is out of
+ * range is left out as described at each call and recorded as
+ * VPP_ERR_INVALID in the status word.
+ * q, k and v are given with their token stride in elements (a multiple of 8,
+ * at least heads x d), so they may be parts of one fused projection
+ * [total_q][heads dq + kv_heads dq + kv_heads dv]; out, lse and the caches
+ * are contiguous.  heads / kv_heads is any whole number from 1 to 16.
+ */
+
+/*
+ * Rotate and append ([VPP review] §2.1: prefill fills the cache that later
+ * chunks and decode read; [GLM PP note] §1: 64-token blocks).
+ *
+ * Sequence b owns packed rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1, which
+ * are its LAST q_len_b positions of ctx_lens[b] (ctx_lens NULL: of q_len_b,
+ * whole prompts).  cu_seqlens_q [batch+1] and ctx_lens [batch] are DEVICE
+ * int32.  A token at position n turns the pairs (x, y) of its query and key
+ * vectors by row n of cos_sin, DEVICE float32 [table_rows][rot_dim] (rot_dim/2
+ * cosines, then rot_dim/2 sines; the caller folds any scaling of the angles
+ * into it):  x' = x cos - y sin,  y' = y cos + x sin.  The rotated dims are
+ * [rot_start, rot_start + rot_dim); pair i is dims (i, i + rot_dim/2) of them,
+ * or (2i, 2i + 1) with interleaved != 0.  Other dims are copied.  The products
+ * are float32 and a result is rounded once (to bf16, or to its E4M3 code).
+ *
+ * q [total_q][heads][head_dim_qk], k [..][kv_heads][head_dim_qk] and
+ * v [..][kv_heads][head_dim_v] are bf16.  The rotated queries go to q_out
+ * (token stride q_out_stride; q_out == q with the same stride rotates in
+ * place; q NULL: keys only), the rotated keys to position n of the paged cache
+ * and, unless k_out is NULL, to k_out (in place likewise), the values to the
+ * cache.  k_cache and v_cache both NULL: rotation only, k_out is then required
+ * and block_table and v are not read.  Other overlaps of inputs and outputs
+ * are not allowed, and two sequences must not share the block of a new token.
+ *
+ * Rows from cu_seqlens_q[batch] to total_q - 1, and the rows of a sequence
+ * with ctx_lens[b] == 0, are padding: nothing is read or written for them.
+ * Nothing is written, and VPP_ERR_INVALID is recorded, for a token whose
+ * position is outside the table, whose block is outside the pool or the block
+ * table's row, or whose ctx_lens[b] < q_len_b, and for rows past total_q.
+ * head_dim_qk and head_dim_v are multiples of 64 up to 512; rot_dim a multiple
+ * of 16 (0: no rotation, cos_sin may be NULL), rot_start of 8.
+ * total_q == 0 is a no-op (pointers may then be NULL).
+ */
+int vpp_rope_append(const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const void *v, int64_t v_stride,
+                    const float *cos_sin, int32_t table_rows, int rot_start,
+                    int rot_dim, int interleaved, void *q_out,
+                    int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                    void *k_cache, void *v_cache, const int32_t *block_table,
+                    int32_t max_blocks_per_seq, int32_t num_blocks,
+                    const int32_t *cu_seqlens_q, const int32_t *ctx_lens,
+                    int32_t batch, int64_t total_q, int heads, int kv_heads,
+                    int head_dim_qk, int head_dim_v, void *stream);
+
+/*
+ * The same into an E4M3 cache (see the fp8 conventions above): a rotated key
+ * or a value x becomes code = E4M3(fl32(x / scale)), the float32 rotation
+ * rounded once.  The caches are required.
+ */
+int vpp_rope_append_fp8(const void *q, int64_t q_stride, const void *k,
+                        int64_t k_stride, const void *v, int64_t v_stride,
+                        const float *cos_sin, int32_t table_rows,
+                        int rot_start, int rot_dim, int interleaved,
+                        void *q_out, int64_t q_out_stride, void *k_out,
+                        int64_t k_out_stride, void *k_cache, void *v_cache,
+                        const float *k_scale, const float *v_scale,
+                        const int32_t *block_table,
+                        int32_t max_blocks_per_seq, int32_t num_blocks,
+                        const int32_t *cu_seqlens_q, const int32_t *ctx_lens,
+                        int32_t batch, int64_t total_q, int heads,
+                        int kv_heads, int head_dim_qk, int head_dim_v,
+                        void *stream);
+
+/*
+ * Decode attention: one new token per sequence over a paged cache ([VPP
+ * review] §2.1, §2.2 Eq. (1)), split over the cache's length and joined
+ * through the LSE ([GLM PP note] §7).
+ *
+ * q [batch][heads][head_dim_qk] bf16 (row stride q_stride).  Row b attends to
+ * keys 0 .. ctx_lens[b]-1 of block-table row b (DEVICE int32 [batch] and
+ * [batch][max_blocks_per_seq]); ctx_lens[b] counts the row's own token, which
+ * must already be in the cache.  A row with ctx_lens[b] == 0 (padding) gets
+ * out = 0 and lse = -inf, and so does one whose length is negative or longer
+ * than its block-table row, which is recorded as VPP_ERR_INVALID.  A block
+ * outside the pool reads as zeros and is recorded as VPP_ERR_INVALID.  Cache
+ * rows past a sequence's length may hold anything.
+ * out [batch][heads][head_dim_v] bf16, lse [heads][batch] float32 (NULL
+ * allowed).  head dims as in the conventions, any number of kv heads.
+ * The keys are dealt out evenly over the GPU, so where a row is split depends
+ * on the other rows' lengths: a row's result may differ in its last bits from
+ * one batch to another (never from run to run).
+ * workspace: DEVICE, 16-byte aligned, vpp_decode_attn_workspace_size(...)
+ * bytes, holding anything; calls that overlap on the GPU, replayed graphs
+ * among them, need one each.
+ */
+int vpp_decode_attn(const void *q, int64_t q_stride, const void *k_cache,
+                    const void *v_cache, const int32_t *block_table,
+                    int32_t max_blocks_per_seq, int32_t num_blocks,
+                    const int32_t *ctx_lens, int32_t batch, int heads,
+                    int kv_heads, int head_dim_qk, int head_dim_v,
+                    float softmax_scale, void *out, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* The same over an E4M3 cache with per-kv-head scales. */
+int vpp_decode_attn_fp8(const void *q, int64_t q_stride, const void *k_cache,
+                        const void *v_cache, const float *k_scale,
+                        const float *v_scale, const int32_t *block_table,
+                        int32_t max_blocks_per_seq, int32_t num_blocks,
+                        const int32_t *ctx_lens, int32_t batch, int heads,
+                        int kv_heads, int head_dim_qk, int head_dim_v,
+                        float softmax_scale, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of vpp_decode_attn / _fp8 (independent of the lengths). */
+size_t vpp_decode_attn_workspace_size(int32_t batch, int heads, int kv_heads,
+                                      int head_dim_qk, int head_dim_v);
+
+/*
+ * Prompt attention: causal self-attention of whole prompts packed one after
+ * the other, read straight from the (rotated) projection, without a cache
+ * ([VPP review] §2.2 Eq. (1)).
+ *
+ * Sequence b owns rows cu_seqlens[b] .. cu_seqlens[b+1]-1 (DEVICE int32
+ * [batch+1]) of q [total_q][heads][head_dim_qk], k [..][kv_heads][head_dim_qk]
+ * and v [..][kv_heads][head_dim_v] (bf16, token strides in elements); its
+ * token i attends to its tokens <= i.  Any number of sequences, empty ones
+ * among them, in one launch.  Rows of no sequence are not written, and what
+ * they and other sequences hold never reaches a result; within a sequence k
+ * and v must be finite (a non-finite value of a later token may reach the
+ * earlier ones of its 128-token tile).  A sequence whose range is not within
+ * 0 .. total_q or ends before it begins is left out and recorded as
+ * VPP_ERR_INVALID.
+ * out [total_q][heads][head_dim_v] bf16, lse [heads][total_q] float32 (NULL
+ * allowed).  workspace: DEVICE, 16-byte aligned,
+ * vpp_prompt_attn_workspace_size(...) bytes, holding anything; calls that
+ * overlap on the GPU need one each.  total_q == 0 is a no-op.
+ */
+int vpp_prompt_attn(const void *q, int64_t q_stride, const void *k,
+                    int64_t k_stride, const void *v, int64_t v_stride,
+                    const int32_t *cu_seqlens, int32_t batch, int64_t total_q,
+                    int heads, int kv_heads, int head_dim_qk, int head_dim_v,
+                    float softmax_scale, void *out, float *lse,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of vpp_prompt_attn (independent of the lengths). */
+size_t vpp_prompt_attn_workspace_size(int32_t batch, int64_t total_q,
+                                      int heads, int kv_heads);
+
+/*
  * Device status word: synchronises `stream`, stores the first error any
  * kernel of this library recorded since the last reset (VPP_OK if none) in
  * *code, and resets the word to VPP_OK.  Returns VPP_ERR_CUDA if the

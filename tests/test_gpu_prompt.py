@@ -1,0 +1,176 @@
+"""Packed prompt attention against the formula in 64 bits: head shapes,
+lengths around the tile edges, empty and invalid sequences, hostile
+neighbours, strided operands, captured calls."""
+
+import pytest
+import torch
+
+from chunked_prefill_causal_gb300 import vpp
+from tests.serving_ref import HALF_BF16, attend, check_attention, randn
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def views(x, H, Hkv, dq, dv):
+    q, k, v = x.split([H * dq, Hkv * dq, Hkv * dv], dim=1)
+    return q.unflatten(1, (H, dq)), k.unflatten(1, (Hkv, dq)), v.unflatten(1, (Hkv, dv))
+
+
+def starts(lens):
+    return torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+
+
+def check_sequences(out, lse, q, k, v, cu, dq, scale=None):
+    for b in range(len(cu) - 1):
+        lo, hi = int(cu[b]), int(cu[b + 1])
+        if hi > lo:
+            ref = attend(q[lo:hi], k[lo:hi], v[lo:hi], scale or dq ** -0.5, True)
+            check_attention(out[lo:hi], None if lse is None else lse[:, lo:hi], ref, dq, HALF_BF16, f"sequence {b} ({hi - lo} tokens)")
+
+
+LENS = [1, 0, 2, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 0, 255, 257, 400]
+SHAPES = [
+    # H, Hkv, dq, dv
+    (8, 2, 128, 128), (4, 4, 128, 128), (16, 1, 128, 128), (6, 2, 64, 64), (5, 1, 64, 128), (14, 2, 128, 64),
+    (3, 3, 192, 128), (12, 1, 192, 64), (8, 1, 64, 64), (26, 2, 128, 128), (22, 2, 192, 128), (30, 2, 64, 64), (2, 1, 192, 128),
+]
+
+
+@pytest.mark.parametrize("H,Hkv,dq,dv", SHAPES)
+def test_matches_formula(H, Hkv, dq, dv):
+    cu = starts(LENS)
+    T = int(cu[-1]) + 5
+    x = randn((T, H * dq + Hkv * (dq + dv)), 1)
+    q, k, v = views(x, H, Hkv, dq, dv)
+    out = torch.full((T, H, dv), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((H, T), 7.0, device=DEV)
+    vpp.vpp_prompt_attn(*views(x.to(DEV), H, Hkv, dq, dv), cu.to(DEV), out=out, lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    check_sequences(out, lse, q, k, v, cu, dq)
+    assert bool((out[int(cu[-1]):] == 7).all()) and bool((lse[:, int(cu[-1]):] == 7).all()), "rows of no sequence written"
+
+
+@pytest.mark.parametrize("lens", [[1], [128], [3, 1500], [1] * 300, [2000], [0, 0, 5, 0], [513, 700, 1, 1, 1025]])
+def test_batch_shapes(lens):
+    H, Hkv, d = 8, 2, 128
+    cu = starts(lens)
+    q, k, v = randn((int(cu[-1]), H, d), 2), randn((int(cu[-1]), Hkv, d), 3), randn((int(cu[-1]), Hkv, d), 4)
+    lse = torch.empty((H, int(cu[-1])), device=DEV)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    check_sequences(out, lse, q, k, v, cu, d)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("H,Hkv,d", [(8, 2, 128), (6, 2, 64), (2, 2, 128)])
+def test_neighbours_never_reach_a_result(H, Hkv, d, bad):
+    """Sequences of hostile values before and behind each good one, and in the rows of no sequence."""
+    lens = [30, 100, 40, 129, 10, 200, 3]
+    cu = starts(lens)
+    T = int(cu[-1]) + 9
+    q, k, v = randn((T, H, d), 5), randn((T, Hkv, d), 6), randn((T, Hkv, d), 7)
+    good = [1, 3, 5]
+    for b in range(len(lens)):
+        if b not in good:
+            for x in (q, k, v):
+                x[int(cu[b]):int(cu[b + 1])] = bad
+    for x in (q, k, v):
+        x[int(cu[-1]):] = bad
+    lse = torch.empty((H, T), device=DEV)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse)
+    for b in good:
+        lo, hi = int(cu[b]), int(cu[b + 1])
+        ref = attend(q[lo:hi], k[lo:hi], v[lo:hi], d ** -0.5, True)
+        check_attention(out[lo:hi], lse[:, lo:hi], ref, d, HALF_BF16, f"sequence {b}")
+
+
+def test_scale_and_no_lse():
+    H, Hkv, d = 4, 2, 64
+    cu = starts([100, 30])
+    q, k, v = randn((130, H, d), 8), randn((130, Hkv, d), 9), randn((130, Hkv, d), 10)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), softmax_scale=0.4)
+    check_sequences(out, None, q, k, v, cu, d, scale=0.4)
+
+
+def test_invalid_ranges_are_left_out_and_reported():
+    H, Hkv, d = 4, 2, 64
+    q, k, v = randn((100, H, d), 11), randn((100, Hkv, d), 12), randn((100, Hkv, d), 13)
+    for cu in ([0, 40, 30, 100], [0, 40, 60, 200], [-20, 10, 50, 100], [0, 40, 1 << 30, 100]):
+        out = torch.full((100, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
+        vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV), out=out)
+        assert vpp.vpp_last_device_status() == vpp.VPP_ERR_INVALID, cu
+        rest = torch.ones(100, dtype=torch.bool)
+        for lo, hi in zip(cu, cu[1:]):
+            if 0 <= lo <= hi <= 100:
+                rest[lo:hi] = False
+        assert bool((out.cpu()[rest] == 7).all()), cu
+    # a valid sequence beside the invalid ones is served
+    cu = [0, 40, 60, 200]
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV))
+    check_sequences(out, None, q, k, v, cu[:3], d)
+    assert vpp.vpp_last_device_status() == vpp.VPP_ERR_INVALID
+
+
+def test_equals_the_cached_path():
+    """A whole prompt through the paged cache and through the packed call: the same attention."""
+    H, Hkv, d, n = 16, 4, 128, 700
+    q, k, v = (randn((n, h, d), 14 + h).to(DEV) for h in (H, Hkv, Hkv))
+    cu = torch.tensor([0, n], dtype=torch.int32)
+    table = torch.arange((n + 63) // 64, dtype=torch.int32, device=DEV)[None]
+    kc = torch.zeros((table.shape[1], 64, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    vpp.vpp_kv_append_varlen(k, v, kc, vc, table, cu.numpy(), [n])
+    a = vpp.vpp_mixed_attn(q, kc, vc, table, cu.numpy(), [n])
+    b = vpp.vpp_prompt_attn(q, k, v, cu.to(DEV))
+    check_sequences(b, None, q.cpu(), k.cpu(), v.cpu(), cu, d)
+    check_sequences(a, None, q.cpu(), k.cpu(), v.cpu(), cu, d)
+
+
+def test_runs_give_the_same_bits_and_a_dirty_workspace_is_fine():
+    H, Hkv, d = 8, 2, 128
+    lens = [300, 1, 77, 512, 0, 64]
+    cu = starts(lens)
+    T = int(cu[-1])
+    q, k, v = randn((T, H, d), 15).to(DEV), randn((T, Hkv, d), 16).to(DEV), randn((T, Hkv, d), 17).to(DEV)
+    ws = torch.empty(vpp.prompt_attn_workspace_size(len(lens), T, H, Hkv) + 16, dtype=torch.uint8, device=DEV)
+    want = vpp.vpp_prompt_attn(q, k, v, cu.to(DEV))
+    for fill in (0, 127, 255):
+        ws.fill_(fill)
+        assert torch.equal(vpp.vpp_prompt_attn(q, k, v, cu.to(DEV), workspace=ws), want)
+
+
+def test_captured_call_follows_the_lengths():
+    H, Hkv, d, T = 8, 2, 128, 900
+    q, k, v = randn((T, H, d), 18), randn((T, Hkv, d), 19), randn((T, Hkv, d), 20)
+    qd, kd, vd = q.to(DEV), k.to(DEV), v.to(DEV)
+    cu = torch.zeros(7, dtype=torch.int32, device=DEV)
+    out, lse = torch.empty((T, H, d), dtype=torch.bfloat16, device=DEV), torch.empty((H, T), device=DEV)
+    ws = torch.empty(vpp.prompt_attn_workspace_size(6, T, H, Hkv) + 16, dtype=torch.uint8, device=DEV)
+    vpp.vpp_prompt_attn(qd, kd, vd, cu, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        vpp.vpp_prompt_attn(qd, kd, vd, cu, out=out, lse=lse, workspace=ws)
+    for lens in ([900, 0, 0, 0, 0, 0], [100] * 6, [1, 2, 3, 4, 5, 6], [0, 0, 0, 0, 0, 900], [450, 300, 50, 60, 39, 1]):
+        now = starts(lens)
+        cu.copy_(now)
+        out.fill_(7.0)
+        graph.replay()
+        check_sequences(out, lse, q, k, v, now, d)
+        assert bool((out[int(now[-1]):] == 7).all())
+    assert vpp.vpp_last_device_status() == 0
+
+
+def test_another_stream():
+    H, Hkv, d = 8, 2, 128
+    cu = starts([500, 30, 200])
+    q, k, v = (randn((730, h, d), 21 + h).to(DEV) for h in (H, Hkv, Hkv))
+    want = vpp.vpp_prompt_attn(q, k, v, cu.to(DEV))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    cud = cu.to(DEV)
+    torch.cuda.synchronize()
+    got = [vpp.vpp_prompt_attn(q, k, v, cud, stream=s) for _ in range(10) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in got)
