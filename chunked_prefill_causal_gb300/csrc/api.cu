@@ -1194,6 +1194,23 @@ int rope_append_impl(bool fp8, RopeParams p, int interleaved, cudaStream_t st) {
   return launch_rope_append(p, interleaved != 0, fp8, ds->num_sms, st) == cudaSuccess ? VPP_OK : VPP_ERR_CUDA;
 }
 
+// A paged cache for the decode kernel: boxes of `rows` tokens of one kv head,
+// one slab wide (64 bf16 values; 128 codes, or 64 where d is no multiple of
+// 128), swizzled by the slab's row width.
+int make_decode_map(CUtensorMap* m, const void* cache, int32_t num_blocks, int kv_heads, int d, bool fp8, int rows) {
+  const cuuint64_t esz = fp8 ? 1 : 2;
+  const cuuint32_t width = fp8 && d % 128 == 0 ? 128 : 64;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)kv_heads, (cuuint64_t)kBlockTokens, (cuuint64_t)num_blocks};
+  const cuuint64_t strides[3] = {d * esz, kv_heads * d * esz, kBlockTokens * kv_heads * d * esz};
+  const cuuint32_t box[4] = {width, 1, (cuuint32_t)rows, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                              const_cast<void*>(cache), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              width * esz == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? VPP_OK : VPP_ERR_INVALID;
+}
+
 int decode_attn_impl(bool fp8, PagedDecodeParams p, float softmax_scale, void* workspace, size_t workspace_bytes,
                      cudaStream_t st) {
   if (p.batch < 0) return VPP_ERR_INVALID;
@@ -1206,7 +1223,9 @@ int decode_attn_impl(bool fp8, PagedDecodeParams p, float softmax_scale, void* w
       !aligned4(p.ctx) || !aligned4(p.lse))
     return VPP_ERR_INVALID;
   if (p.max_blocks_per_seq <= 0 || p.num_blocks <= 0) return VPP_ERR_INVALID;
-  if ((int64_t)p.max_blocks_per_seq * kBlockTokens > INT32_MAX) return VPP_ERR_INVALID;
+  if ((int64_t)p.max_blocks_per_seq * kBlockTokens > INT32_MAX ||
+      (int64_t)p.max_blocks_per_seq * p.batch > INT32_MAX)
+    return VPP_ERR_INVALID;
   if (fp8 && !scales_ok(p.k_scale, p.v_scale)) return VPP_ERR_INVALID;
   DeviceState* ds = nullptr;
   if (int r = device_state(&ds)) return r;
@@ -1214,7 +1233,13 @@ int decode_attn_impl(bool fp8, PagedDecodeParams p, float softmax_scale, void* w
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return VPP_ERR_WORKSPACE;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)p.dq)) * 1.4426950408889634f;
   p.status = ds->status;
-  return launch_paged_decode(p, fp8, workspace, ds->num_sms, st) == cudaSuccess ? VPP_OK : VPP_ERR_CUDA;
+  CUtensorMap maps[4];
+  if (make_decode_map(&maps[0], p.k_cache, p.num_blocks, p.kv_heads, p.dq, fp8, kBlockTokens) ||
+      make_decode_map(&maps[1], p.v_cache, p.num_blocks, p.kv_heads, p.dv, fp8, kBlockTokens) ||
+      make_decode_map(&maps[2], p.k_cache, p.num_blocks, p.kv_heads, p.dq, fp8, 16) ||
+      make_decode_map(&maps[3], p.v_cache, p.num_blocks, p.kv_heads, p.dv, fp8, 16))
+    return VPP_ERR_INVALID;
+  return launch_paged_decode(p, fp8, maps, workspace, ds->num_sms, st) == cudaSuccess ? VPP_OK : VPP_ERR_CUDA;
 }
 
 }  // namespace

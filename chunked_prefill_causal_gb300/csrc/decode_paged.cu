@@ -6,6 +6,45 @@
 // accumulated cache) and §2.2, Eq. (1), for a query at position ctx - 1:
 //     out = sum_j exp(s_j - L) v_j,   s_j = scale q . k_j,   L = ln sum_j exp(s_j)
 // over keys 0 .. ctx - 1, evaluated online (running max and denominator).
+//
+// Bound by HBM: every cached key and value is read once and used for the G
+// query heads of its kv head only.
+//
+// Work split.  The pages (64-token blocks) of all sequences, in order, form
+// one list of N pages.  It is cut into `cols` equal parts whatever the
+// lengths are; CTA (column c, kv head h) takes pages [c N / cols,
+// (c + 1) N / cols) of head h.  cols x kv_heads fills the SMs (two CTAs each)
+// in whole waves, so the launch shape needs no length and every CTA reads the
+// same number of pages.  The CTAs of one column are neighbours in launch order and
+// read the same blocks at the same time, head by head.  A sequence
+// inside one column is finished there; one that crosses columns leaves a
+// float32 partial (sum, max, denominator) per column, which decode_join_kernel adds up
+// ("02 · 并行策略与 PP 切分" note, §7).  A column has at most two such
+// sequences, its first and its last.
+//
+// CTA (160 threads):
+//   warp 4      producer: one TMA box of 64 tokens x 64 dims (128 codes) per
+//               slab of a page's K and V into a ring of stages; the
+//               last page of a sequence in boxes of 16 tokens, so that a short
+//               sequence does not read 64 rows for a few.  It looks up the
+//               block table 32 pages at a time.
+//   warps 0-3   tokens 16 w .. 16 w + 15 of the page: S = Q K^T and O += P V on
+//               the warp-level tensor cores (mma.sync m16n8k16, float32
+//               accumulation).  The 16 rows are the group's query heads (zeros past
+//               G), K and V come by ldmatrix from the swizzled stage, and P
+//               goes from the accumulators of S to the operand of P V in
+//               registers.  The decode products need a few per cent of even this
+//               tensor path; tcgen05's 128-row tiles would be 1/8 to 1/128 full.
+// The four warps' running results are joined through shared memory at the end
+// of each sequence.
+//
+// E4M3 cache: the codes are widened exactly to f16 operands (every E4M3 value
+// is an f16 value) after ldmatrix; q is scaled per head by a power of two into f16's
+// range; k_scale joins the score scale and v_scale the result.
+#include <algorithm>
+
+#include <cuda.h>
+
 #include "ptx.cuh"
 #include "serve.cuh"
 
@@ -13,71 +52,724 @@ namespace vpp {
 namespace {
 
 constexpr float kLn2p = 0.69314718055994530942f;
+constexpr int kConsumers = 4;
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kCtasPerSm = 2;
+constexpr int kRingBytes = 96 * 1024;
 
-template <bool F8>
-__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
-  if (F8) {
-    uint32_t lo, hi;
-    e4m3x4_to_f16x2x2(static_cast<const uint8_t*>(p)[i], lo, hi);
-    float f;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(f) : "r"(lo));
-    return f;
-  }
-  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
+template <int DQ, int DV, bool F8>
+struct Cfg {
+  static constexpr int ESZ = F8 ? 1 : 2;
+  // Bytes of a slab row: 64 bf16 values, 128 codes (or 64 where the head dim
+  // is no multiple of 128).
+  static constexpr int KROW = F8 ? (DQ % 128 == 0 ? 128 : 64) : 128;
+  static constexpr int VROW = F8 ? (DV % 128 == 0 ? 128 : 64) : 128;
+  static constexpr int KSLABS = DQ * ESZ / KROW;
+  static constexpr int VSLABS = DV * ESZ / VROW;
+  static constexpr int KBYTES = DQ * ESZ * kBlockTokens;
+  static constexpr int STAGE = KBYTES + DV * ESZ * kBlockTokens;
+  static constexpr int NST = kRingBytes / STAGE > 8 ? 8 : kRingBytes / STAGE;
+  static constexpr int KS = DQ / 16;  // k-steps of S
+  static constexpr int NT = DV / 8;   // 8-dim tiles of O
+  static constexpr int CSTRIDE = DV + 4;  // row stride of the join buffer: at most 2 lanes on a bank
+  static constexpr int COMB = kConsumers * 8 * CSTRIDE * 4;
+  static constexpr int SMEM = NST * STAGE + COMB + kConsumers * 8 * 8 + 2 * NST * 8 + 48;
+  static_assert(NST >= 2, "two stages at least");
+  static_assert(SMEM + 1024 <= 228 * 1024 / kCtasPerSm, "two CTAs per SM");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
-// One warp per (row, head); a lane holds dims lane + 32 i.
-template <bool F8>
-__global__ void __launch_bounds__(128) paged_decode_kernel(const __grid_constant__ PagedDecodeParams p) {
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+// D (16 x 8, f32) += A (16 x 16) B (16 x 8), f16 or bf16 operands.
+template <bool F16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Byte offset of 16-byte chunk c of row r in a slab that TMA wrote with the
+// swizzle of its row width (128 or 64 bytes).
+template <int ROW>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return ROW == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// One thing the join kernel adds up: the parts of sequence b in columns
+// c - 1 (slot `slot`) and c .. c + n - 2 (slot 0), filed under column c.
+struct JoinDesc {
+  int32_t b;  // -1: none
+  int32_t n;
+  int32_t slot;
+  int32_t pad;
+};
+
+struct Workspace {
+  float* o;      // [cols][2][heads][dv], sums relative to 2^max
+  float2* ml;    // [cols][2][heads], (max, denominator)
+  JoinDesc* desc;  // [cols]
+};
+
+// A context length as the kernels use it: 0 for one that does not fit its
+// block-table row.
+__device__ __forceinline__ int valid_ctx(const PagedDecodeParams& p, int ctx) {
+  return (ctx < 0 || ctx > p.max_blocks_per_seq * kBlockTokens) ? 0 : ctx;
+}
+__device__ __forceinline__ int pages_of(int ctx) { return (ctx + kBlockTokens - 1) / kBlockTokens; }
+
+// Walks the non-empty sequences from one on; every lane of the warp holds one
+// of 32 lengths, so a run of empty rows costs one load per 32.
+struct SeqWalk {
+  int base;  // first sequence of the lanes
+  int mine;  // this lane's length
+  int b;     // current sequence
+  int ctx;
+  __device__ __forceinline__ void load(const PagedDecodeParams& p, int from) {
+    base = from;
+    const int i = from + (threadIdx.x & 31);
+    mine = i < p.batch ? valid_ctx(p, __ldg(p.ctx + i)) : 0;
+  }
+  __device__ __forceinline__ void start(const PagedDecodeParams& p, int at) {
+    load(p, at);
+    b = at;
+    ctx = __shfl_sync(0xffffffffu, mine, 0);
+  }
+  // Goes on to the next non-empty sequence (there is one).
+  __device__ __forceinline__ void next(const PagedDecodeParams& p) {
+    int from = b - base + 1;
+    while (true) {
+      const uint32_t live = from < 32 ? __ballot_sync(0xffffffffu, mine > 0) & (0xffffffffu << from) : 0u;
+      if (live) {
+        const int l = __ffs(live) - 1;
+        b = base + l;
+        ctx = __shfl_sync(0xffffffffu, mine, l);
+        return;
+      }
+      if (base + 32 >= p.batch) return;  // not reached while pages are left
+      load(p, base + 32);
+      from = 0;
+    }
+  }
+};
+
+template <int DQ, int DV, bool F8>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
+                        const __grid_constant__ PagedDecodeParams p, const Workspace ws, const int cols) {
+  using C = Cfg<DQ, DV, F8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float* comb = reinterpret_cast<float*>(smem + C::NST * C::STAGE);                  // [4][8][CSTRIDE]
+  float2* ml = reinterpret_cast<float2*>(smem + C::NST * C::STAGE + C::COMB);        // [4][8]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ml + kConsumers * 8);                 // full[NST], empty[NST]
+  volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(bars + 2 * C::NST);
+  int* scan = reinterpret_cast<int*>(const_cast<uint32_t*>(abort_flag) + 1);         // 5 sums, then (b, page)
+  const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  if (w >= static_cast<int64_t>(p.batch) * p.heads) return;
-  const int b = static_cast<int>(w / p.heads), h = static_cast<int>(w % p.heads);
-  const int g = h / (p.heads / p.kv_heads);
-  int ctx = __ldg(p.ctx + b);
-  if (ctx < 0 || ctx > static_cast<int64_t>(p.max_blocks_per_seq) * kBlockTokens) {
-    if (lane == 0) record_status(p.status, kStatusInvalid);
-    ctx = 0;
+  const int col = blockIdx.x / p.kv_heads;
+  const int h = blockIdx.x - col * p.kv_heads;
+  const int G = p.heads / p.kv_heads;
+
+  // The join kernel may be placed beside this one; it waits for its end.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0u;
+    for (int i = 0; i < C::NST; ++i) {
+      mbar_init(smem_u32(&bars[i]), 1);
+      mbar_init(smem_u32(&bars[C::NST + i]), kConsumers);
+    }
+    fence_mbar_init();
   }
-  float q[6], o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < p.dq / 32; ++i)
-    q[i] = __uint_as_float(static_cast<uint32_t>(p.q[b * p.q_stride + h * p.dq + lane + 32 * i]) << 16);
-  const float sl = F8 ? p.scale_log2 * __ldg(p.k_scale + g) : p.scale_log2;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < ctx; ++j) {
-    const int32_t blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq + j / kBlockTokens);
-    const bool ok = blk >= 0 && blk < p.num_blocks;
-    if (!ok && lane == 0) record_status(p.status, kStatusInvalid);
-    const int64_t row = (static_cast<int64_t>(blk) * kBlockTokens + j % kBlockTokens) * p.kv_heads + g;
-    float s = 0.f;
-    for (int i = 0; i < p.dq / 32; ++i) s += ok ? q[i] * load_elem<F8>(p.k_cache, row * p.dq + lane + 32 * i) : 0.f;
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= sl;
-    const float mn = fmaxf(m, s), f = ex2_approx(m - mn), e = ex2_approx(s - mn);
-    m = mn;
-    l = l * f + e;
-    for (int i = 0; i < p.dv / 32; ++i)
-      o[i] = o[i] * f + (ok ? e * load_elem<F8>(p.v_cache, row * p.dv + lane + 32 * i) : 0.f);
+  // ---- this column's pages: warp w adds up the w-th fifth of the sequences,
+  // and the one whose range holds the column's first page finds it.
+  const int per = (p.batch + 4) / 5;
+  const int b0 = min(p.batch, warp * per), b1 = min(p.batch, b0 + per);
+  int sum = 0;
+  for (int b = b0 + lane; b < b1; b += 32) {
+    const int raw = __ldg(p.ctx + b);
+    const int c = valid_ctx(p, raw);
+    if (c != raw && blockIdx.x == 0) record_status(p.status, kStatusInvalid);
+    sum += pages_of(c);
   }
-  const float inv = l > 0.f ? (F8 ? __ldg(p.v_scale + g) : 1.f) / l : 0.f;
-  for (int i = 0; i < p.dv / 32; ++i)
-    p.out[(static_cast<int64_t>(b) * p.heads + h) * p.dv + lane + 32 * i] =
-        static_cast<uint16_t>(pack_bf16x2(o[i] * inv, 0.f) & 0xFFFF);
-  if (p.lse && lane == 0) p.lse[static_cast<int64_t>(h) * p.batch + b] = l > 0.f ? m * kLn2p + logf(l) : -INFINITY;
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) scan[warp] = sum;
+  __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < 5; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  const int nc = min(cols, total);  // columns with pages: at least one page each
+  const int first = col < nc ? static_cast<int>(static_cast<int64_t>(col) * total / nc) : 0;
+  const int last = col < nc ? static_cast<int>(static_cast<int64_t>(col + 1) * total / nc) : 0;  // one past
+  __syncthreads();
+  if (first < last && first >= before && first < before + sum) {
+    int at = before;
+    for (int b = b0;; b += 32) {
+      const int n = b + lane < b1 ? pages_of(valid_ctx(p, __ldg(p.ctx + b + lane))) : 0;
+      int inc = n;  // inclusive prefix over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, first < at + inc);
+      if (hit) {
+        if (lane == __ffs(hit) - 1) {
+          scan[5] = b + lane;
+          scan[6] = first - (at + inc - n);
+        }
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  __syncthreads();
+  const int n_pages = last - first;
+  const int start_b = n_pages > 0 ? scan[5] : 0;
+  const int start_page = n_pages > 0 ? scan[6] : 0;  // pages of start_b before this column
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------ producer
+    if (h == 0 && lane == 0) {
+      // File the sequence that column col - 1 ends with and this one goes on
+      // with, if it began there: the parts of one sequence are one entry.
+      JoinDesc d{-1, 0, 0, 0};
+      if (n_pages > 0 && start_page > 0) {
+        const int begin = first - start_page;  // the sequence's first page
+        const int prev = static_cast<int>(static_cast<int64_t>(col - 1) * total / nc);
+        if (begin >= prev) {
+          const int64_t end = begin + pages_of(valid_ctx(p, __ldg(p.ctx + start_b)));  // one past
+          const int last_col = static_cast<int>((end * nc - 1) / total);
+          d = JoinDesc{start_b, last_col - col + 2, begin == prev ? 0 : 1, 0};
+        }
+      }
+      if (cols > 1) ws.desc[col] = d;
+    }
+    if (n_pages > 0) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      // Starts the copies of a page with `rest` tokens of its sequence left.
+      auto copy_page = [&](int slot, int32_t blk, int rest) {
+        const uint32_t full = smem_u32(&bars[slot]);
+        const uint32_t dk = smem_u32(smem + slot * C::STAGE), dv = dk + C::KBYTES;
+        if (rest > kBlockTokens - 16) {
+          mbar_arrive_expect_tx(full, C::STAGE);
+#pragma unroll
+          for (int s = 0; s < C::KSLABS; ++s)
+            tma_load_4d(dk + s * C::KROW * kBlockTokens, &tm_k, full, s * (C::KROW / C::ESZ), h, 0, blk);
+#pragma unroll
+          for (int s = 0; s < C::VSLABS; ++s)
+            tma_load_4d(dv + s * C::VROW * kBlockTokens, &tm_v, full, s * (C::VROW / C::ESZ), h, 0, blk);
+        } else {
+          const int groups = (rest + 15) / 16;
+          mbar_arrive_expect_tx(full, groups * (C::STAGE / 4));
+          for (int g = 0; g < groups; ++g) {
+            for (int s = 0; s < C::KSLABS; ++s)
+              tma_load_4d(dk + (s * kBlockTokens + 16 * g) * C::KROW, &tm_k16, full, s * (C::KROW / C::ESZ), h,
+                          16 * g, blk);
+            for (int s = 0; s < C::VSLABS; ++s)
+              tma_load_4d(dv + (s * kBlockTokens + 16 * g) * C::VROW, &tm_v16, full, s * (C::VROW / C::ESZ), h,
+                          16 * g, blk);
+          }
+        }
+      };
+      SeqWalk sw;
+      sw.start(p, start_b);
+      int page = start_page, left = n_pages;
+      int slot = 0;
+      uint32_t phase = 0u, filled = 0u, fill_phase = 0u;
+      bool ok = true;
+      while (ok && left > 0) {
+        const int np = min(pages_of(sw.ctx) - page, left);
+        const int32_t* row = p.block_table + static_cast<int64_t>(sw.b) * p.max_blocks_per_seq + page;
+        int32_t next_blk = lane < np ? __ldg(row + lane) : 0;
+        for (int i = 0; ok && i < np; i += 32) {
+          const int32_t blks = next_blk;  // lane l: block of page i + l
+          // the next 32 entries load while these pages are copied
+          next_blk = i + 32 + lane < np ? __ldg(row + i + 32 + lane) : 0;
+          const int live = min(32, np - i);
+          for (int j = 0; j < live; ++j) {
+            int32_t blk = __shfl_sync(0xffffffffu, blks, j);
+            if (blk < 0 || blk >= p.num_blocks) {
+              if (lane == 0) record_status(p.status, kStatusInvalid);
+              blk = p.num_blocks;  // out of the map: reads zeros
+            }
+            if (lane == 0) {
+              ok = mbar_wait(smem_u32(&bars[C::NST + slot]), phase ^ 1u, p.status, abort_flag);
+              if (ok) copy_page(slot, blk, sw.ctx - (page + i + j) * kBlockTokens);
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+            filled |= 1u << slot;
+            fill_phase = (fill_phase & ~(1u << slot)) | (phase << slot);
+            if (++slot == C::NST) {
+              slot = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        left -= np;
+        page = 0;
+        if (left > 0) sw.next(p);
+      }
+      if (!ok && lane == 0) {
+        // Let every copy land before the CTA exits.
+        for (int i = 0; i < C::NST; ++i)
+          if (filled & (1u << i)) mbar_wait_for(smem_u32(&bars[i]), (fill_phase >> i) & 1u, 100000000ull);
+      }
+    }
+    return;
+  }
+
+  // -------------------------------------------------------- consumers
+  // Rows of length 0: zeros, and -inf for the log of an empty sum.
+  for (int b = col; b < p.batch; b += cols) {
+    if (valid_ctx(p, __ldg(p.ctx + b)) > 0) continue;
+    uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * p.heads + h * G) * DV);
+    for (int i = threadIdx.x; i < G * DV / 8; i += 32 * kConsumers) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse && threadIdx.x < G) p.lse[static_cast<int64_t>(h * G + threadIdx.x) * p.batch + b] = -INFINITY;
+  }
+  if (n_pages == 0) return;
+
+  const int g = lane >> 2, u = lane & 3;  // fragment row and column pair
+  const int mi = lane >> 3, r8 = lane & 7;  // matrix and row that this lane addresses in ldmatrix
+  const float sl = F8 ? p.scale_log2 * __ldg(p.k_scale + h) : p.scale_log2;
+  const float vsc = F8 ? __ldg(p.v_scale + h) : 1.f;
+  const uint32_t ring = smem_u32(smem);
+  // rows of this lane's ldmatrix addresses: K pairs (token half, chunk), V
+  // pairs (chunk, token half); codes pair (chunk, token half) in both
+  const int krow = warp * 16 + (F8 ? (mi & 1) : (mi >> 1)) * 8 + r8;
+  const int vrow = warp * 16 + (mi & 1) * 8 + r8;
+
+  SeqWalk sw;
+  sw.start(p, start_b);
+  int page = start_page, left = n_pages;
+  int slot = 0;
+  uint32_t phase = 0u;
+  bool ok = true;
+  while (left > 0) {
+    const int seq_pages = pages_of(sw.ctx);
+    const int np = min(seq_pages - page, left);
+    // ---- q of the sequence as the A operand: rows g and g + 8
+    uint32_t qa[C::KS][4];
+    float rs[2] = {sl, sl};  // score scale of the two rows
+    {
+      const uint16_t* qrow = p.q + sw.b * p.q_stride + static_cast<int64_t>(h) * G * DQ;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool live = g + 8 * r < G;
+        const uint16_t* src = qrow + (live ? g + 8 * r : 0) * DQ;
+        if (!F8) {
+#pragma unroll
+          for (int s = 0; s < C::KS; ++s) {
+            const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u));
+            const uint32_t hi = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u + 8));
+            qa[s][r] = live ? lo : 0u;
+            qa[s][2 + r] = live ? hi : 0u;
+          }
+        } else {
+          // codes 4u .. 4u + 3 of a 16-dim step are a lane's (see the K
+          // operand), and the row is scaled by 2^e so that its largest |q| is in
+          // [2^14, 2^15): below f16's largest value, and every bf16 value that is
+          // not negligible beside it keeps its 8 significant bits
+          const uint2* src4 = reinterpret_cast<const uint2*>(src + 4 * u);
+          float amax = 0.f;
+#pragma unroll
+          for (int s = 0; s < C::KS; ++s) {
+            const uint2 w = __ldg(src4 + 4 * s);
+            qa[s][r] = live ? w.x : 0u;
+            qa[s][2 + r] = live ? w.y : 0u;
+            amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))),
+                                     fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y)))));
+          }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const int e = (amax > 0.f && amax < INFINITY) ? max(-60, min(60, 14 - ilogbf(amax))) : 0;
+          const float up = ldexpf(1.f, e);
+          rs[r] = sl * ldexpf(1.f, -e);
+#pragma unroll
+          for (int s = 0; s < C::KS; ++s) {
+            qa[s][r] = pack_half2(bf16_lo(qa[s][r]) * up, bf16_hi(qa[s][r]) * up);
+            qa[s][2 + r] = pack_half2(bf16_lo(qa[s][2 + r]) * up, bf16_hi(qa[s][2 + r]) * up);
+          }
+        }
+      }
+    }
+    float m[2] = {-INFINITY, -INFINITY};
+    float l[2] = {0.f, 0.f};  // this lane's part of the denominators
+    float o[C::NT][4];
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+
+    for (int i = 0; i < np; ++i) {
+      // tokens of this warp's 16 that are keys of the sequence
+      const int live = sw.ctx - (page + i) * kBlockTokens - warp * 16;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[slot]), phase, p.status, abort_flag));
+      if (ok && live > 0) {
+        const uint32_t kb = ring + slot * C::STAGE, vb = kb + C::KBYTES;
+        // ---- S = Q K^T: two 8-token tiles, two accumulator chains each
+        float s[2][2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) s[t][c][0] = s[t][c][1] = s[t][c][2] = s[t][c][3] = 0.f;
+        if (!F8) {
+#pragma unroll
+          for (int k = 0; k < C::KS; ++k) {
+            uint32_t r[4];
+            ldsm4(kb + (k >> 2) * 128 * kBlockTokens + swz<128>(krow, 2 * (k & 3) + (mi & 1)), r);
+            mma<false>(s[0][k & 1], qa[k], r[0], r[1]);
+            mma<false>(s[1][k & 1], qa[k], r[2], r[3]);
+          }
+        } else {
+          constexpr int CPS = C::KROW / 16;  // 16-code chunks of a slab row
+#pragma unroll
+          for (int k = 0; k < C::KS; k += 2) {
+            uint32_t r[4], lo, hi;
+            ldsm4(kb + (k / CPS) * C::KROW * kBlockTokens + swz<C::KROW>(krow, k % CPS + (mi >> 1)), r);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              e4m3x4_to_f16x2x2(r[x], lo, hi);
+              mma<true>(s[x & 1][x >> 1], qa[k + (x >> 1)], lo, hi);
+            }
+          }
+        }
+        // ---- scores in log2 units; keys past the sequence leave the softmax
+        float sc[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = (s[t][0][e] + s[t][1][e]) * rs[e >> 1];
+            sc[t][e] = 8 * t + 2 * u + (e & 1) < live ? v : -INFINITY;
+          }
+        // ---- online softmax of rows g and g + 8 (four lanes hold a row); the
+        // reference moves only when the maximum has grown by more than 2^8
+        float f[2];
+        bool moved = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          f[r] = 1.f;
+          if (mx > m[r] + 8.0f || (m[r] == -INFINITY && mx > -INFINITY)) {
+            f[r] = ex2_approx(m[r] - mx);
+            m[r] = mx;
+            moved = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+          l[0] *= f[0];
+          l[1] *= f[1];
+#pragma unroll
+          for (int n = 0; n < C::NT; ++n) {
+            o[n][0] *= f[0];
+            o[n][1] *= f[0];
+            o[n][2] *= f[1];
+            o[n][3] *= f[1];
+          }
+        }
+        uint32_t pa[4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float mr = m[r] == -INFINITY ? 0.f : m[r];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float a = ex2_approx(sc[t][2 * r] - mr), b = ex2_approx(sc[t][2 * r + 1] - mr);
+            l[r] += a + b;
+            // P is rounded to the operand type of V; the denominator keeps float32
+            pa[2 * t + r] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
+          }
+        }
+        // ---- O += P V.  Rows past the sequence may hold anything, and P = 0
+        // times them must stay 0: their halves of the operand words are cleared.
+        uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+        if (live < 16) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int at = 8 * t + 2 * u;
+            mask[t] = (at < live ? 0x0000FFFFu : 0u) | (at + 1 < live ? 0xFFFF0000u : 0u);
+          }
+        }
+        if (!F8) {
+#pragma unroll
+          for (int n = 0; n < C::NT; n += 2) {
+            uint32_t r[4];
+            ldsm4_t(vb + (n >> 3) * 128 * kBlockTokens + swz<128>(vrow, (n & 7) + (mi >> 1)), r);
+            mma<false>(o[n], pa, r[0] & mask[0], r[1] & mask[1]);
+            mma<false>(o[n + 1], pa, r[2] & mask[0], r[3] & mask[1]);
+          }
+        } else {
+          // A word holds dims 2g, 2g + 1 of tokens 2u, 2u + 1: tile n takes the
+          // even dims of a 16-dim chunk, tile n + 1 the odd ones.
+          constexpr int CPS = C::VROW / 16;
+#pragma unroll
+          for (int c = 0; c < DV / 16; c += 2) {
+            uint32_t r[4];
+            ldsm4_t(vb + (c / CPS) * C::VROW * kBlockTokens + swz<C::VROW>(vrow, c % CPS + (mi >> 1)), r);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t e0, d0, e1, d1;
+              e4m3x4_to_f16x2x2(__byte_perm(r[2 * x] & mask[0], 0u, 0x3120u), e0, d0);
+              e4m3x4_to_f16x2x2(__byte_perm(r[2 * x + 1] & mask[1], 0u, 0x3120u), e1, d1);
+              mma<true>(o[2 * (c + x)], pa, e0, e1);
+              mma<true>(o[2 * (c + x) + 1], pa, d0, d1);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars[C::NST + slot]));
+      if (++slot == C::NST) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    }
+
+    // ---- join the four warps, 8 rows at a time.  Every warp comes here for
+    // every sequence, also after a failed wait, so the barriers match.
+    const bool whole = np == seq_pages;
+    const int part = (col * 2 + (page == start_page && left == n_pages ? 0 : 1));
+    for (int half = 0; half < (G > 8 ? 2 : 1); ++half) {
+      float lr = l[half];
+      lr += __shfl_xor_sync(0xffffffffu, lr, 1);
+      lr += __shfl_xor_sync(0xffffffffu, lr, 2);
+      if (u == 0) ml[warp * 8 + g] = make_float2(m[half], lr);
+      float* dst = comb + (warp * 8 + g) * C::CSTRIDE;
+      if (!F8) {
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+          *reinterpret_cast<float2*>(dst + 8 * n + 2 * u) =
+              half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
+      } else {
+#pragma unroll
+        for (int n = 0; n < C::NT; n += 2)
+          *reinterpret_cast<float4*>(dst + 8 * n + 4 * u) =
+              half ? make_float4(o[n][2], o[n + 1][2], o[n][3], o[n + 1][3])
+                   : make_float4(o[n][0], o[n + 1][0], o[n][1], o[n + 1][1]);
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      constexpr int PER = DV / 16;  // dims of a thread: 16 threads a row
+      const int r = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * PER;
+      if (r + 8 * half < G) {
+        float wgt[kConsumers], top = -INFINITY, den = 0.f;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) top = fmaxf(top, ml[w * 8 + r].x);
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float2 x = ml[w * 8 + r];
+          wgt[w] = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+          den += wgt[w] * x.y;
+        }
+        float acc[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+          const float* src = comb + (w * 8 + r) * C::CSTRIDE + d0;
+#pragma unroll
+          for (int i = 0; i < PER; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src + i);
+            acc[i] += wgt[w] * x.x;
+            acc[i + 1] += wgt[w] * x.y;
+            acc[i + 2] += wgt[w] * x.z;
+            acc[i + 3] += wgt[w] * x.w;
+          }
+        }
+        const int hq = h * G + 8 * half + r;
+        if (whole) {
+          const float inv = den > 0.f ? vsc / den : (den == den ? 0.f : den);  // a NaN stays one
+          uint16_t* out = p.out + (static_cast<int64_t>(sw.b) * p.heads + hq) * DV + d0;
+          uint32_t pk[PER / 2];
+#pragma unroll
+          for (int i = 0; i < PER / 2; ++i) pk[i] = pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+          if (PER == 8)
+            *reinterpret_cast<uint4*>(out) = make_uint4(pk[0], pk[1], pk[2 % (PER / 2)], pk[3 % (PER / 2)]);
+          else
+            *reinterpret_cast<uint2*>(out) = make_uint2(pk[0], pk[1]);
+          if (p.lse && d0 == 0)
+            p.lse[static_cast<int64_t>(hq) * p.batch + sw.b] = den > 0.f ? top * kLn2p + logf(den) : (den == den ? -INFINITY : den);
+        } else {
+          const int64_t at = static_cast<int64_t>(part) * p.heads + hq;
+#pragma unroll
+          for (int i = 0; i < PER; i += 4)
+            *reinterpret_cast<float4*>(ws.o + at * DV + d0 + i) =
+                make_float4(acc[i] * vsc, acc[i + 1] * vsc, acc[i + 2] * vsc, acc[i + 3] * vsc);
+          if (d0 == 0) ws.ml[at] = make_float2(top, den);
+        }
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+    left -= np;
+    page = 0;
+    if (left > 0) sw.next(p);
+  }
 }
+
+// Adds up the parts of one sequence that crosses columns, for one query head:
+// CTA (column, head); warp w takes parts w, w + 4, ...
+template <int DV>
+__global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant__ PagedDecodeParams p,
+                                                          const Workspace ws) {
+  constexpr int PER = DV / 32;
+  __shared__ float so[4][DV];
+  __shared__ float2 sml[4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, hq = blockIdx.y;
+  const JoinDesc d = ws.desc[c];
+  if (d.b < 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto at = [&](int i) {
+    return static_cast<int64_t>(i == 0 ? (c - 1) * 2 + d.slot : (c - 1 + i) * 2) * p.heads + hq;
+  };
+  float m = -INFINITY, l = 0.f, acc[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) acc[j] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < d.n; i += 4) {
+    const float2 x = ws.ml[at(i)];
+    float v[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] = ws.o[at(i) * DV + lane + 32 * j];
+    const float top = fmaxf(m, x.x);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - top), w = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+    l = l * f + x.y * w;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) acc[j] = acc[j] * f + v[j] * w;
+    m = top;
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) so[warp][lane + 32 * j] = acc[j];
+  if (lane == 0) sml[warp] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x >= DV) return;
+  float top = -INFINITY, den = 0.f, x = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, sml[w].x);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = sml[w].x == -INFINITY ? 0.f : ex2_approx(sml[w].x - top);
+    den += f * sml[w].y;
+    x += f * so[w][threadIdx.x];
+  }
+  const float inv = den > 0.f ? 1.f / den : (den == den ? 0.f : den);
+  p.out[(static_cast<int64_t>(d.b) * p.heads + hq) * DV + threadIdx.x] =
+      static_cast<uint16_t>(pack_bf16x2(x * inv, 0.f) & 0xFFFFu);
+  if (p.lse && threadIdx.x == 0)
+    p.lse[static_cast<int64_t>(hq) * p.batch + d.b] = den > 0.f ? top * kLn2p + logf(den) : (den == den ? -INFINITY : den);
+}
+
+// Columns of the work split: cols x kv_heads CTAs in whole waves of the CTAs
+// that are resident at once.  The smallest number of waves that leaves at most 4%
+// of the places empty (8 kv heads: one wave of 38 columns; 128: three
+// waves of 7), or the fullest of up to four.
+int decode_cols(int kv_heads, int num_sms) {
+  const int places = kCtasPerSm * num_sms;
+  int best = 1;
+  double best_fill = 0.0;
+  for (int w = 1; w <= 4; ++w) {
+    const int c = w * places / kv_heads;
+    if (c < 1) continue;
+    const double fill = static_cast<double>(c) * kv_heads / (w * places);
+    if (fill > best_fill + 1e-9) {
+      best_fill = fill;
+      best = c;
+    }
+    if (best_fill >= 0.96) break;
+  }
+  return best;
+}
+
+template <int DQ, int DV, bool F8>
+cudaError_t launch_t(const PagedDecodeParams& p, const CUtensorMap* maps, const Workspace& ws, int cols,
+                     cudaStream_t stream) {
+  using C = Cfg<DQ, DV, F8>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static bool configured[64] = {};
+  if (dev < 64 && !configured[dev]) {
+    e = cudaFuncSetAttribute(paged_decode_kernel<DQ, DV, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  paged_decode_kernel<DQ, DV, F8><<<cols * p.kv_heads, kThreads, C::SMEM, stream>>>(maps[0], maps[1], maps[2], maps[3],
+                                                                                  p, ws, cols);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || cols == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(cols, p.heads);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_join_kernel<DV>, p, ws);
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t paged_decode_ws_bytes(int32_t, int, int, int, int, int) { return 0; }
+size_t paged_decode_ws_bytes(int32_t, int heads, int kv_heads, int, int dv, int num_sms) {
+  const size_t cols = decode_cols(kv_heads, num_sms);
+  if (cols == 1) return 0;
+  return align256(cols * 2 * heads * dv * 4) + align256(cols * 2 * heads * 8) + align256(cols * sizeof(JoinDesc));
+}
 
-cudaError_t launch_paged_decode(const PagedDecodeParams& p, bool fp8, void*, int, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(p.batch) * p.heads;
-  const int grid = static_cast<int>((warps + 3) / 4);
-  if (fp8)
-    paged_decode_kernel<true><<<grid, 128, 0, stream>>>(p);
-  else
-    paged_decode_kernel<false><<<grid, 128, 0, stream>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, bool fp8, const CUtensorMap* maps, void* workspace,
+                                int num_sms, cudaStream_t stream) {
+  const int cols = decode_cols(p.kv_heads, num_sms);
+  Workspace ws = {};
+  if (cols > 1) {
+    uint8_t* at = static_cast<uint8_t*>(workspace);
+    ws.o = reinterpret_cast<float*>(at);
+    at += align256(static_cast<size_t>(cols) * 2 * p.heads * p.dv * 4);
+    ws.ml = reinterpret_cast<float2*>(at);
+    at += align256(static_cast<size_t>(cols) * 2 * p.heads * 8);
+    ws.desc = reinterpret_cast<JoinDesc*>(at);
+  }
+#define VPP_CASE(DQ, DV)                                                             \
+  if (p.dq == DQ && p.dv == DV)                                                      \
+    return fp8 ? launch_t<DQ, DV, true>(p, maps, ws, cols, stream)                   \
+               : launch_t<DQ, DV, false>(p, maps, ws, cols, stream);
+  VPP_CASE(64, 64)
+  VPP_CASE(64, 128)
+  VPP_CASE(128, 64)
+  VPP_CASE(128, 128)
+  VPP_CASE(192, 64)
+  VPP_CASE(192, 128)
+#undef VPP_CASE
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace vpp

@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -59,8 +60,9 @@ struct PagedDecodeParams {
 };
 
 size_t paged_decode_ws_bytes(int32_t batch, int heads, int kv_heads, int dq, int dv, int num_sms);
-cudaError_t launch_paged_decode(const PagedDecodeParams& p, bool fp8, void* workspace, int num_sms,
-                                cudaStream_t stream);
+// maps: K and V of the cache in boxes of 64 tokens, then in boxes of 16.
+cudaError_t launch_paged_decode(const PagedDecodeParams& p, bool fp8, const CUtensorMap* maps, void* workspace,
+                                int num_sms, cudaStream_t stream);
 
 // Packed prompt attention (prompt_attn.cu).
 struct PromptParams {

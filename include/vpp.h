@@ -503,7 +503,8 @@ int vpp_rope_append_fp8(const void *q, int64_t q_stride, const void *k,
  * outside the pool reads as zeros and is recorded as VPP_ERR_INVALID.  Cache
  * rows past a sequence's length may hold anything.
  * out [batch][heads][head_dim_v] bf16, lse [heads][batch] float32 (NULL
- * allowed).  head dims as in the conventions, any number of kv heads.
+ * allowed).  head dims as in the conventions, kv_heads up to 1024,
+ * batch x max_blocks_per_seq below 2^31.
  * The keys are dealt out evenly over the GPU, so where a row is split depends
  * on the other rows' lengths: a row's result may differ in its last bits from
  * one batch to another (never from run to run).
