@@ -1163,6 +1163,23 @@ bool strided_ok(const void* p, int64_t stride, int64_t row) {
 
 constexpr int64_t kMaxPackedRows = INT32_MAX / 2;
 
+// Packed q: a box is 64 dims x G heads x 1 kv head x floor(128 / G) tokens.
+int make_packed_q_map(CUtensorMap* m, const void* q, int64_t stride, int64_t total_q, int heads, int kv_heads, int dq) {
+  const int G = heads / kv_heads;
+  const cuuint64_t dims[4] = {(cuuint64_t)dq, (cuuint64_t)G, (cuuint64_t)kv_heads, (cuuint64_t)total_q};
+  const cuuint64_t strides[3] = {(cuuint64_t)dq * 2, (cuuint64_t)G * dq * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)(kTileM / G)};
+  return encode_map(m, q, 4, dims, strides, box);
+}
+
+// Packed k or v: boxes of 64 tokens; rows past total_q read zeros.
+int make_packed_kv_map(CUtensorMap* m, const void* x, int64_t stride, int64_t total_q, int kv_heads, int d) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)kv_heads, (cuuint64_t)total_q};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)kBlockTokens};
+  return encode_map(m, x, 3, dims, strides, box);
+}
+
 int rope_append_impl(bool fp8, RopeParams p, int interleaved, cudaStream_t st) {
   if (p.total_q < 0 || p.total_q > kMaxPackedRows || p.batch < 0) return VPP_ERR_INVALID;
   if (p.total_q == 0) return VPP_OK;  // pointers may be NULL without rows
@@ -1319,19 +1336,36 @@ int vpp_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_st
   if (!out || !aligned16(out) || !aligned4(lse)) return VPP_ERR_INVALID;
   DeviceState* ds = nullptr;
   if (int r = device_state(&ds)) return r;
-  const size_t need = prompt_ws_bytes(batch, total_q, heads, kv_heads);
-  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return VPP_ERR_WORKSPACE;
+  CUtensorMap tm_q, tm_k, tm_v;
+  if (make_packed_q_map(&tm_q, q, q_stride, total_q, heads, kv_heads, head_dim_qk) ||
+      make_packed_kv_map(&tm_k, k, k_stride, total_q, kv_heads, head_dim_qk) ||
+      make_packed_kv_map(&tm_v, v, v_stride, total_q, kv_heads, head_dim_v))
+    return VPP_ERR_INVALID;
+  PackedParams p = {};
+  p.heads = heads;
+  p.kv_heads = kv_heads;
+  p.group = heads / kv_heads;
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)head_dim_qk);
-  const PromptParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
-                       static_cast<const uint16_t*>(v), cu_seqlens, static_cast<uint16_t*>(out), lse,
-                       q_stride, k_stride, v_stride, total_q, batch, heads, kv_heads, head_dim_qk, head_dim_v,
-                       scale * 1.4426950408889634f, ds->status};
-  return launch_prompt_attn(p, workspace, ds->num_sms, as_stream(stream)) == cudaSuccess ? VPP_OK : VPP_ERR_CUDA;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.lse_stride = total_q;
+  p.status = ds->status;
+  p.cu = cu_seqlens;
+  p.batch = batch;
+  p.total = total_q;
+  // At most total / 2T whole pairs and one partial pair per sequence.
+  const int64_t items = total_q / (2 * (kTileM / p.group)) + std::min<int64_t>(batch, total_q);
+  if (items * kv_heads > INT32_MAX) return VPP_ERR_INVALID;
+  return launch_packed_attn(head_dim_qk, head_dim_v, tm_q, tm_k, tm_v, p, (int)(items * kv_heads), as_stream(stream)) ==
+                 cudaSuccess
+             ? VPP_OK
+             : VPP_ERR_CUDA;
 }
 
 size_t vpp_prompt_attn_workspace_size(int32_t batch, int64_t total_q, int heads, int kv_heads) {
   if (batch <= 0 || total_q <= 0 || total_q > kMaxPackedRows || check_groups(heads, kv_heads)) return 0;
-  return prompt_ws_bytes(batch, total_q, heads, kv_heads);
+  return 0;
 }
 
 int vpp_last_device_status(void* stream, int* code) {

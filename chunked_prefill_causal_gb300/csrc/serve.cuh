@@ -1,5 +1,5 @@
 // serve.cuh -- parameters of the serving-step kernels whose lengths live on
-// the device (rotate-and-append, decode attention, packed prompt attention),
+// the device (rotate-and-append, decode attention),
 // shared with api.cu.
 #pragma once
 
@@ -63,25 +63,6 @@ size_t paged_decode_ws_bytes(int32_t batch, int heads, int kv_heads, int dq, int
 // maps: K and V of the cache in boxes of 64 tokens, then in boxes of 16.
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, bool fp8, const CUtensorMap* maps, void* workspace,
                                 int num_sms, cudaStream_t stream);
-
-// Packed prompt attention (prompt_attn.cu).
-struct PromptParams {
-  const uint16_t* q;  // bf16 [total_q][heads][dq], token stride q_stride
-  const uint16_t* k;
-  const uint16_t* v;
-  const int32_t* cu;  // [batch + 1]
-  uint16_t* out;      // bf16 [total_q][heads][dv]
-  float* lse;         // [heads][total_q], may be null
-  int64_t q_stride, k_stride, v_stride;
-  int64_t total_q;
-  int32_t batch;
-  int32_t heads, kv_heads, dq, dv;
-  float scale_log2;
-  int* status;
-};
-
-size_t prompt_ws_bytes(int32_t batch, int64_t total_q, int heads, int kv_heads);
-cudaError_t launch_prompt_attn(const PromptParams& p, void* workspace, int num_sms, cudaStream_t stream);
 
 // The sequence that owns packed row t: the last b with cu[b] <= t (0 when
 // there is none; the caller checks t against the sequence's range).
