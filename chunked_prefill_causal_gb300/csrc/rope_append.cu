@@ -16,15 +16,16 @@
 //
 // Bound by HBM for many tokens (each input is read and each output written
 // once), by the latency of the chain lengths -> block and table row -> stores
-// for few.
+// for few.  Measured on a GB300: 16384 tokens of 64 + 8 heads of 128, 679 MB,
+// in 104.5 us (6.5 TB/s, 96% of the copy bandwidth); 4 decode tokens in 3.1 us.
 //
-// Work split.  A row (one head of one token) is d / 16 tasks of two 16-byte vectors:
-// eight pairs of the rotated dims (both ends of the pairs, so that one thread
-// holds them whole and rotation in place is safe), or 16 copied values.  A
-// thread keeps its task for every row of a token, so the eight cosines and
-// sines are loaded once for all heads, and four rows are in flight at once.
-// A CTA takes a few consecutive tokens and looks up their positions and slots
-// side by side, one thread a token, while the first rows load.
+// Work split.  A row (one head of one token) is d / 16 tasks of two 16-byte
+// vectors: eight pairs of the rotated dims (both ends of the pairs, so that one
+// thread holds them whole and rotation in place is safe), or 16 copied values.
+// A token is served by 64 threads of a CTA, or by all 256 when there are few
+// tokens.  A thread keeps its task for every row of the token, so the eight
+// cosines and sines are loaded once for all heads; two rows are in flight at
+// once, the first ones while the token's position and slot are looked up.
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -34,8 +35,10 @@ namespace vpp {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kMaxTile = 4;  // tokens of a CTA
-constexpr int kRows = 4;     // rows in flight per thread
+constexpr int kRopeCtas = 4;  // CTAs per SM
+constexpr int kMaxTile = 4;   // tokens of a CTA (a power of two)
+constexpr int kRows = 2;      // rows in flight per thread
+constexpr int kRopeWaves = 4;  // waves of CTAs to aim at
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -109,19 +112,33 @@ __device__ __forceinline__ Place place_of(const RopeParams& p, int64_t t) {
   return Place{row, static_cast<int32_t>(pos)};
 }
 
+// Rotates the eight pairs of a task in float32.
+template <bool IL>
+__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (&cs)[8], const float (&sn)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // pair e: (x_e, y_e), or interleaved (x_2e, x_2e+1) for e < 4, then y's
+    float& u = !IL ? x[e] : e < 4 ? x[2 * e] : y[2 * e - 8];
+    float& v = !IL ? y[e] : e < 4 ? x[2 * e + 1] : y[2 * e - 7];
+    const float a = u, b = v;
+    u = fmaf(a, cs[e], -__fmul_rn(b, sn[e]));
+    v = fmaf(b, cs[e], __fmul_rn(a, sn[e]));
+  }
+}
+
 template <bool IL, bool F8>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const __grid_constant__ RopeParams p,
-                                                                      const int tile) {
-  __shared__ Place places[kMaxTile];
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * tile;
-  const int nt = static_cast<int>(min(static_cast<int64_t>(tile), p.total_q - t0));
-  if (static_cast<int>(threadIdx.x) < nt) places[threadIdx.x] = place_of(p, t0 + threadIdx.x);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && __ldg(p.cu + p.batch) > p.total_q) record_status(p.status, kStatusInvalid);
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(const __grid_constant__ RopeParams p,
+                                                                              const int tile) {
+  // Thread i of the token's `wide` threads.
+  const int wide = kRopeThreads / tile;
+  const int i = threadIdx.x % wide;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * tile + threadIdx.x / wide;
+  if (t >= p.total_q) return;
 
   // This thread's task of a query or key row: vectors at dims d0 and d1, and
   // the first of its eight angles (-1: copied).
   const int per = p.dq / 16;  // tasks of a row
-  const int c = threadIdx.x % per, first = threadIdx.x / per, step = kRopeThreads / per;
+  const int c = i % per, first = i / per, step = wide / per;
   const int rot = p.rot_dim / 16;
   int d0, d1, angle = -1;
   if (c < rot) {
@@ -134,113 +151,98 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const __gr
     d1 = 8 * (v + 1) + (v + 1 < head ? 0 : p.rot_dim);
   }
   const int hq = p.q ? p.heads : 0;
-  const int rows = hq + p.kv_heads;
-  __syncthreads();
-
-  for (int i = 0; i < nt; ++i) {
-    const Place at = places[i];
-    if (at.pos < 0) continue;
-    const int64_t t = t0 + i;
-    float cs[8], sn[8];
-    if (angle >= 0) {
-      const float4* src = reinterpret_cast<const float4*>(p.cos_sin + static_cast<int64_t>(at.pos) * p.rot_dim + angle);
-      const float4 c0 = __ldg(src), c1 = __ldg(src + 1);
-      const float4* src2 = reinterpret_cast<const float4*>(p.cos_sin + static_cast<int64_t>(at.pos) * p.rot_dim +
-                                                           p.rot_dim / 2 + angle);
-      const float4 s0 = __ldg(src2), s1 = __ldg(src2 + 1);
-      cs[0] = c0.x; cs[1] = c0.y; cs[2] = c0.z; cs[3] = c0.w; cs[4] = c1.x; cs[5] = c1.y; cs[6] = c1.z; cs[7] = c1.w;
-      sn[0] = s0.x; sn[1] = s0.y; sn[2] = s0.z; sn[3] = s0.w; sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
-    }
-    const uint16_t* qs = p.q + t * p.q_stride;
-    const uint16_t* ks = p.k + t * p.k_stride;
-    // (threads past the last whole group of `per` have no task)
-    for (int r0 = first; first < step && r0 < rows; r0 += kRows * step) {
-      uint4 a[kRows], b[kRows];
+  // (threads past the last whole group of `per` have no row)
+  const int rows = first < step ? hq + p.kv_heads : 0;
+  const uint16_t* qs = p.q + t * p.q_stride;
+  const uint16_t* ks = p.k + t * p.k_stride - static_cast<int64_t>(hq) * p.dq;
+  uint4 a[kRows], b[kRows];
+  auto load = [&](int r0) {
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        const int r = r0 + j * step;
-        if (r < rows) {
-          const uint16_t* src = r < hq ? qs + r * p.dq : ks + (r - hq) * p.dq;
-          a[j] = ld_once(src + d0);
-          b[j] = ld_once(src + d1);
-        }
+    for (int j = 0; j < kRows; ++j) {
+      const int r = r0 + j * step;
+      if (r < rows) {
+        const uint16_t* src = (r < hq ? qs : ks) + r * p.dq;
+        a[j] = ld_once(src + d0);
+        b[j] = ld_once(src + d1);
       }
+    }
+  };
+  // gridDim.y CTAs share a token's rows, kRows passes at a time.
+  const int begin = first + blockIdx.y * kRows * step, stride = gridDim.y * kRows * step;
+  load(begin);  // in flight while the token's place is looked up
+
+  if (t == 0 && i == 0 && blockIdx.y == 0 && __ldg(p.cu + p.batch) > p.total_q) record_status(p.status, kStatusInvalid);
+  const Place at = place_of(p, t);
+  if (at.pos < 0) return;
+  float cs[8], sn[8];
+  if (angle >= 0) {
+    const float* src = p.cos_sin + static_cast<int64_t>(at.pos) * p.rot_dim + angle;
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        const int r = r0 + j * step;
-        if (r >= rows) continue;
-        float x[8], y[8];
+    for (int e = 0; e < 8; e += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(src + e));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(src + p.rot_dim / 2 + e));
+      cs[e] = x.x; cs[e + 1] = x.y; cs[e + 2] = x.z; cs[e + 3] = x.w;
+      sn[e] = y.x; sn[e + 1] = y.y; sn[e + 2] = y.z; sn[e + 3] = y.w;
+    }
+  }
+  for (int r0 = begin; r0 < rows; r0 += stride) {
+    if (r0 != begin) load(r0);
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const int r = r0 + j * step;
+      if (r >= rows) continue;
+      float x[8], y[8];
+      if (angle >= 0 || F8) {
         unpack8(a[j], x);
         unpack8(b[j], y);
-        if (angle >= 0) {
-          if (IL) {  // pairs (x0, x1), ..., (y6, y7)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float u = x[2 * e], v = x[2 * e + 1], w = y[2 * e], z = y[2 * e + 1];
-              x[2 * e] = __fsub_rn(__fmul_rn(u, cs[e]), __fmul_rn(v, sn[e]));
-              x[2 * e + 1] = __fadd_rn(__fmul_rn(v, cs[e]), __fmul_rn(u, sn[e]));
-              y[2 * e] = __fsub_rn(__fmul_rn(w, cs[4 + e]), __fmul_rn(z, sn[4 + e]));
-              y[2 * e + 1] = __fadd_rn(__fmul_rn(z, cs[4 + e]), __fmul_rn(w, sn[4 + e]));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float u = x[e], v = y[e];
-              x[e] = __fsub_rn(__fmul_rn(u, cs[e]), __fmul_rn(v, sn[e]));
-              y[e] = __fadd_rn(__fmul_rn(v, cs[e]), __fmul_rn(u, sn[e]));
-            }
-          }
-        }
-        if (r < hq) {
-          uint16_t* dst = p.q_out + t * p.q_out_stride + r * p.dq;
-          *reinterpret_cast<uint4*>(dst + d0) = pack8(x);
-          *reinterpret_cast<uint4*>(dst + d1) = pack8(y);
-        } else {
-          const int h = r - hq;
-          if (p.k_out || !F8) {
-            const uint4 u = pack8(x), v = pack8(y);
-            if (p.k_out) {
-              uint16_t* dst = p.k_out + t * p.k_out_stride + h * p.dq;
-              *reinterpret_cast<uint4*>(dst + d0) = u;
-              *reinterpret_cast<uint4*>(dst + d1) = v;
-            }
-            if (!F8 && p.k_cache) {
-              uint16_t* dst = static_cast<uint16_t*>(p.k_cache) + (at.row * p.kv_heads + h) * p.dq;
-              *reinterpret_cast<uint4*>(dst + d0) = u;
-              *reinterpret_cast<uint4*>(dst + d1) = v;
-            }
-          }
-          if (F8) {
-            const float scale = __ldg(p.k_scale + h);
-            uint8_t* dst = static_cast<uint8_t*>(p.k_cache) + (at.row * p.kv_heads + h) * p.dq;
-            *reinterpret_cast<uint2*>(dst + d0) = codes8(x, scale);
-            *reinterpret_cast<uint2*>(dst + d1) = codes8(y, scale);
-          }
+      }
+      if (angle >= 0) {
+        turn<IL>(x, y, cs, sn);
+        a[j] = pack8(x);
+        b[j] = pack8(y);
+      }
+      auto put = [&](uint16_t* dst) {
+        *reinterpret_cast<uint4*>(dst + d0) = a[j];
+        *reinterpret_cast<uint4*>(dst + d1) = b[j];
+      };
+      if (r < hq) {
+        put(p.q_out + t * p.q_out_stride + r * p.dq);
+      } else {
+        const int h = r - hq;
+        const int64_t row = (at.row * p.kv_heads + h) * p.dq;
+        if (p.k_out) put(p.k_out + t * p.k_out_stride + h * p.dq);
+        if (F8) {
+          const float scale = __ldg(p.k_scale + h);
+          uint8_t* dst = static_cast<uint8_t*>(p.k_cache) + row;
+          *reinterpret_cast<uint2*>(dst + d0) = codes8(x, scale);
+          *reinterpret_cast<uint2*>(dst + d1) = codes8(y, scale);
+        } else if (p.k_cache) {
+          put(static_cast<uint16_t*>(p.k_cache) + row);
         }
       }
     }
-    if (!p.k_cache) continue;
-    // values: the token's kv heads are contiguous on both sides
-    const uint16_t* vs = p.v + t * p.v_stride;
-    const int n = p.kv_heads * p.dv / 8;
-    for (int e0 = threadIdx.x; e0 < n; e0 += kRows * kRopeThreads) {
-      uint4 a[kRows];
+  }
+  if (!p.k_cache) return;
+  // values: the token's kv heads are contiguous on both sides
+  const uint16_t* vs = p.v + t * p.v_stride;
+  const int64_t row = at.row * p.kv_heads * p.dv;
+  const int n = p.kv_heads * p.dv / 8;
+  for (int e0 = i + blockIdx.y * 2 * kRows * wide; e0 < n; e0 += gridDim.y * 2 * kRows * wide) {
+    uint4 w[2 * kRows];
 #pragma unroll
-      for (int j = 0; j < kRows; ++j)
-        if (e0 + j * kRopeThreads < n) a[j] = ld_once(vs + 8 * (e0 + j * kRopeThreads));
+    for (int j = 0; j < 2 * kRows; ++j)
+      if (e0 + j * wide < n) w[j] = ld_once(vs + 8 * (e0 + j * wide));
 #pragma unroll
-      for (int j = 0; j < kRows; ++j) {
-        const int e = e0 + j * kRopeThreads;
-        if (e >= n) continue;
-        const int64_t dst = at.row * p.kv_heads * p.dv + 8 * e;
-        if (F8) {
-          float x[8];
-          unpack8(a[j], x);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + dst) =
-              codes8(x, __ldg(p.v_scale + 8 * e / p.dv));
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.v_cache) + dst) = a[j];
-        }
+    for (int j = 0; j < 2 * kRows; ++j) {
+      const int e = e0 + j * wide;
+      if (e >= n) continue;
+      if (F8) {
+        float x[8];
+        unpack8(w[j], x);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + row + 8 * e) =
+            codes8(x, __ldg(p.v_scale + 8 * e / p.dv));
+      } else {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.v_cache) + row + 8 * e) = w[j];
       }
     }
   }
@@ -249,9 +251,17 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const __gr
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeParams& p, bool interleaved, bool fp8, int num_sms, cudaStream_t stream) {
-  // One token a CTA until every SM has its three CTAs, then up to kMaxTile.
-  const int tile = static_cast<int>(std::min<int64_t>(kMaxTile, std::max<int64_t>(1, p.total_q / (3 * num_sms))));
-  const int grid = static_cast<int>((p.total_q + tile - 1) / tile);
+  // One token a CTA until every SM has its CTAs, then up to kMaxTile.
+  int tile = 1;
+  while (tile < kMaxTile && p.total_q >= static_cast<int64_t>(2 * tile) * kRopeCtas * num_sms) tile *= 2;
+  // Tokens of many rows are shared by several CTAs while there are fewer than
+  // kRopeWaves waves of them: 800 tokens of 128 + 128 rows of 192 took 22.6 us with
+  // one CTA a token and 21.7 us with several (256 decode tokens: 6.1 and 5.3 us).
+  const int64_t ctas = (p.total_q + tile - 1) / tile;
+  const int pass = kRows * (kRopeThreads / tile / (p.dq / 16));  // rows in flight
+  const int passes = ((p.q ? p.heads : 0) + p.kv_heads + pass - 1) / pass;
+  const int64_t want = (static_cast<int64_t>(kRopeWaves) * kRopeCtas * num_sms + ctas - 1) / ctas;
+  const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(passes, want))));
   if (interleaved)
     fp8 ? rope_append_kernel<true, true><<<grid, kRopeThreads, 0, stream>>>(p, tile)
         : rope_append_kernel<true, false><<<grid, kRopeThreads, 0, stream>>>(p, tile);
