@@ -9,7 +9,9 @@ in the library's CUDA kernels; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -76,8 +78,8 @@ SIGNATURES = {
                              _i32, _int, _int, _int, _int, _f32, _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p], _int),
     "vpp_decode_attn_workspace_size": ([_i32, _int, _int, _int, _int], _sz),
     "vpp_prompt_attn": ([_c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i32, _i64, _int, _int, _int, _int,
-                         _f32, _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p], _int),
-    "vpp_prompt_attn_workspace_size": ([_i32, _i64, _int, _int], _sz),
+                         _f32, _c_void_p, _c_void_p, _c_void_p], _int),
+    "vpp_call": ([_int, ctypes.c_char_p, _int], _int),
     "vpp_last_device_status": ([_c_void_p, ctypes.POINTER(_int)], _int),
     "vpp_selftest_wait_timeout": ([_int, _c_void_p], _int),
 }
@@ -459,45 +461,52 @@ def vpp_topk_chunk_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_len, t
 
 
 # ----------------------------------------------------------------- lengths on the device
-def _on_device(dev, *ts):
+# These calls are a few microseconds of GPU time at decode sizes, so their
+# arguments travel as one packed array of 64-bit words (vpp_call): converting
+# thirty ctypes arguments one by one takes longer than the smallest kernels.
+_OP_ROPE, _OP_ROPE_FP8, _OP_DECODE, _OP_DECODE_FP8, _OP_PROMPT = 1, 2, 3, 4, 5
+_ROPE, _ROPE_FP8 = struct.Struct("=29q"), struct.Struct("=31q")
+_DECODE, _DECODE_FP8, _PROMPT = struct.Struct("=13qf4x5q"), struct.Struct("=15qf4x5q"), struct.Struct("=13qf4x3q")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_ptr(stream, dev):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
+
+
+def _same_device(dev, *ts):
     for t in ts:
         if t is not None and t.get_device() != dev:
             raise ValueError("tensors must be on the current CUDA device")
 
 
-def _rows(t, what, heads=None, d=None):
-    """(pointer, token stride) of a bf16 [tokens, heads, d] tensor whose rows are contiguous (a part of a wider
-    projection is); a stride of one token is never used and reported as the row's length."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{what} is a bf16 [tokens, heads, d] tensor")
-    n, h, w = t.shape
+def _token_stride(t, what, n, h, d):
+    """Token stride in elements of a bf16 [n, h, d] tensor whose heads are contiguous within a token (a part of a wider
+    projection is); the stride of a single token is never used and reported as the row's length."""
+    if t.dtype is not torch.bfloat16 or t.shape != (n, h, d):
+        raise ValueError(f"{what} must be bf16 {[n, h, d]}, not {t.dtype} {list(t.shape)}")
     st, sh, sd = t.stride()
-    if (heads is not None and h != heads) or (d is not None and w != d):
-        raise ValueError(f"{what} has the wrong heads or head dim")
-    if (sd != 1 and w > 1) or (sh != w and h > 1):
+    if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{what}: a token's heads must be contiguous")
-    return t.data_ptr(), st if n > 1 else h * w
+    return st if n > 1 else h * d
 
 
-def _lengths(t, n, what):
-    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what} is a contiguous int32 CUDA tensor of {n} entries")
-    return t.data_ptr()
+def _contiguous(t, what, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} tensor, not {t.dtype} {list(t.shape)}")
 
 
-def _paged(k_cache, v_cache, block_table, batch, dtype):
-    """Checks a paged cache and its block table; (kv_heads, dq, dv)."""
-    if k_cache.dtype is not dtype or v_cache.dtype is not dtype or k_cache.dim() != 4 or v_cache.dim() != 4:
-        raise ValueError(f"caches are {dtype} [num_blocks, 64, kv_heads, d]")
+def _paged_cache(k_cache, v_cache, dtype):
+    """(num_blocks, kv_heads, dq, dv) of a paged cache."""
     nb, bl, hkv, dq = k_cache.shape
-    if bl != 64 or v_cache.shape[:3] != k_cache.shape[:3]:
-        raise ValueError("caches are [num_blocks, 64, kv_heads, d] with the same blocks and heads")
-    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
-        raise ValueError("caches must be contiguous")
-    if (block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch
-            or not block_table.is_contiguous()):
-        raise ValueError("block_table is a contiguous int32 [batch, max_blocks] CUDA tensor")
-    return hkv, dq, v_cache.shape[3]
+    dv = v_cache.shape[3]
+    if bl != 64:
+        raise ValueError("caches are [num_blocks, 64, kv_heads, d]")
+    _contiguous(k_cache, "k_cache", dtype, (nb, 64, hkv, dq))
+    _contiguous(v_cache, "v_cache", dtype, (nb, 64, hkv, dv))
+    return nb, hkv, dq, dv
 
 
 def _empty(shape, dtype, like, stream):
@@ -508,73 +517,63 @@ def _empty(shape, dtype, like, stream):
     return t
 
 
-def _out_lse(out, lse, n, heads, dv, like, stream):
-    if out is None:
-        out = _empty((n, heads, dv), torch.bfloat16, like, stream)
-    elif out.dtype is not torch.bfloat16 or out.shape != (n, heads, dv) or not out.is_contiguous():
-        raise ValueError("out is a contiguous bf16 [tokens, heads, head_dim_v] tensor")
-    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (heads, n) or not lse.is_contiguous()):
-        raise ValueError("lse is a contiguous float32 [heads, tokens] tensor")
-    return out, None if lse is None else lse.data_ptr()
-
-
 def _scratch(workspace, need, like, stream):
     """(tensor, pointer, bytes) of the caller's workspace, or of one allocated for this call."""
     if workspace is None:
         if need == 0:
-            return None, None, 0
+            return None, 0, 0
         workspace = _empty(need, torch.uint8, like, stream)
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _rope_append(name, q, k, v, cos_sin, k_cache, v_cache, scales, block_table, cu_seqlens_q, ctx_lens, q_out, k_out,
+def _call(name, op, form, *words):
+    code = load().vpp_call(op, form.pack(*words), len(words))
+    if code != VPP_OK:
+        raise VppError(name, code)
+
+
+def _rope_append(name, op, q, k, v, cos_sin, k_cache, v_cache, scales, block_table, cu_seqlens_q, ctx_lens, q_out, k_out,
                  rot_start, interleaved, stream):
     dev = torch.cuda.current_device()
-    _on_device(dev, q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_q, ctx_lens, q_out, k_out)
+    _same_device(dev, q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_q, ctx_lens, q_out, k_out, *scales)
     T, Hkv, dq = k.shape
-    kp, ks = _rows(k, "k")
+    ks = _token_stride(k, "k", T, Hkv, dq)
     batch = cu_seqlens_q.shape[0] - 1
-    cu = _lengths(cu_seqlens_q, batch + 1, "cu_seqlens_q")
-    ctx = None if ctx_lens is None else _lengths(ctx_lens, batch, "ctx_lens")
-    vp = vs = dv = qp = qs = H = qop = qos = kop = kos = nb = mb = 0
-    kc = vc = bt = None
+    _contiguous(cu_seqlens_q, "cu_seqlens_q", torch.int32, (batch + 1,))
+    ctx = vp = vs = qp = qs = H = qop = qos = kop = kos = nb = mb = kc = vc = bt = rows = rot = cs = 0
+    dv = 64  # no values without a cache
+    if ctx_lens is not None:
+        _contiguous(ctx_lens, "ctx_lens", torch.int32, (batch,))
+        ctx = ctx_lens.data_ptr()
     if k_cache is not None:
-        kv, kd, dv = _paged(k_cache, v_cache, block_table, batch, torch.uint8 if scales else torch.bfloat16)
-        if (kv, kd) != (Hkv, dq):
+        nb, kv, kd, dv = _paged_cache(k_cache, v_cache, torch.uint8 if scales else torch.bfloat16)
+        if kv != Hkv or kd != dq:
             raise ValueError("k and the key cache have different heads or head dims")
-        vp, vs = _rows(v, "v", Hkv, dv)
-        if v.shape[0] != T:
-            raise ValueError("k and v have different token counts")
-        kc, vc, bt, nb, mb = k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), k_cache.shape[0], block_table.shape[1]
-    else:
-        dv = 64  # no values
+        mb = block_table.shape[1]
+        _contiguous(block_table, "block_table", torch.int32, (batch, mb))
+        vs = _token_stride(v, "v", T, Hkv, dv)
+        vp, kc, vc, bt = v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()
     if q is not None:
         H = q.shape[1]
-        qp, qs = _rows(q, "q", H, dq)
+        qs = _token_stride(q, "q", T, H, dq)
         if q_out is None:
             q_out = _empty((T, H, dq), torch.bfloat16, q, stream)
-        qop, qos = _rows(q_out, "q_out", H, dq)
-        if q.shape[0] != T or q_out.shape[0] != T:
-            raise ValueError("q, q_out and k have different token counts")
+        qos = _token_stride(q_out, "q_out", T, H, dq)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:
-        kop, kos = _rows(k_out, "k_out", Hkv, dq)
-        if k_out.shape[0] != T:
-            raise ValueError("k_out and k have different token counts")
-    rows = rot = 0
-    cs = None
+        kos = _token_stride(k_out, "k_out", T, Hkv, dq)
+        kop = k_out.data_ptr()
     if cos_sin is not None:
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin is a contiguous float32 [positions, rot_dim] tensor")
         rows, rot = cos_sin.shape
+        _contiguous(cos_sin, "cos_sin", torch.float32, (rows, rot))
         cs = cos_sin.data_ptr()
-    head = (qp or None, qs, kp, ks, vp or None, vs, cs, rows, int(rot_start), rot, int(bool(interleaved)), qop or None, qos,
-            kop or None, kos, kc, vc)
-    tail = (bt, mb, nb, cu, ctx, batch, T, H, Hkv, dq, dv, _stream(stream))
-    _check(name, getattr(load(), name)(*head, *scales, *tail))
+    _call(name, op, _ROPE_FP8 if scales else _ROPE, qp, qs, k.data_ptr(), ks, vp, vs, cs, rows, rot_start, rot,
+          1 if interleaved else 0, qop, qos, kop, kos, kc, vc, *[s.data_ptr() for s in scales], bt, mb, nb,
+          cu_seqlens_q.data_ptr(), ctx, batch, T, H, Hkv, dq, dv, _stream_ptr(stream, dev))
     return q_out
 
 
@@ -586,36 +585,43 @@ def vpp_rope_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_
     projection.  cu_seqlens_q, ctx_lens: int32 CUDA tensors, read when the
     kernel runs.  q_out / k_out may be q / k themselves (rotation in place);
     q None rotates keys only; caches, v and block_table None rotate only."""
-    return _rope_append("vpp_rope_append", q, k, v, cos_sin, k_cache, v_cache, (), block_table, cu_seqlens_q, ctx_lens, q_out,
-                        k_out, rot_start, interleaved, stream)
+    return _rope_append("vpp_rope_append", _OP_ROPE, q, k, v, cos_sin, k_cache, v_cache, (), block_table, cu_seqlens_q, ctx_lens,
+                        q_out, k_out, rot_start, interleaved, stream)
 
 
 def vpp_rope_append_fp8(q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, ctx_lens=None,
                         q_out=None, k_out=None, rot_start=0, interleaved=False, stream=None):
     """vpp_rope_append into an E4M3 paged cache (uint8 codes, per-kv-head scales)."""
     _scales(k_scale, v_scale, k.shape[1])
-    _on_device(torch.cuda.current_device(), k_scale, v_scale)
-    return _rope_append("vpp_rope_append_fp8", q, k, v, cos_sin, k_cache, v_cache, (k_scale.data_ptr(), v_scale.data_ptr()),
-                        block_table, cu_seqlens_q, ctx_lens, q_out, k_out, rot_start, interleaved, stream)
+    return _rope_append("vpp_rope_append_fp8", _OP_ROPE_FP8, q, k, v, cos_sin, k_cache, v_cache, (k_scale, v_scale), block_table,
+                        cu_seqlens_q, ctx_lens, q_out, k_out, rot_start, interleaved, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def decode_attn_workspace_size(batch, heads, kv_heads, dq, dv):
     return int(load().vpp_decode_attn_workspace_size(int(batch), heads, kv_heads, dq, dv))
 
 
-def _decode_attn(name, q, k_cache, v_cache, scales, block_table, ctx_lens, out, lse, softmax_scale, workspace, stream):
-    _on_device(torch.cuda.current_device(), q, k_cache, v_cache, block_table, ctx_lens, out, lse, workspace)
+def _decode_attn(name, op, q, k_cache, v_cache, scales, block_table, ctx_lens, out, lse, softmax_scale, workspace, stream):
+    dev = torch.cuda.current_device()
+    _same_device(dev, q, k_cache, v_cache, block_table, ctx_lens, out, lse, workspace, *scales)
     B, H, _ = q.shape
-    Hkv, dq, dv = _paged(k_cache, v_cache, block_table, B, torch.uint8 if scales else torch.bfloat16)
-    qp, qs = _rows(q, "q", H, dq)
-    ctx = _lengths(ctx_lens, B, "ctx_lens")
-    out, lp = _out_lse(out, lse, B, H, dv, q, stream)
-    lib = load()
-    need = lib.vpp_decode_attn_workspace_size(B, H, Hkv, dq, dv) if workspace is None else 0
+    nb, Hkv, dq, dv = _paged_cache(k_cache, v_cache, torch.uint8 if scales else torch.bfloat16)
+    qs = _token_stride(q, "q", B, H, dq)
+    mb = block_table.shape[1]
+    _contiguous(block_table, "block_table", torch.int32, (B, mb))
+    _contiguous(ctx_lens, "ctx_lens", torch.int32, (B,))
+    if out is None:
+        out = _empty((B, H, dv), torch.bfloat16, q, stream)
+    else:
+        _contiguous(out, "out", torch.bfloat16, (B, H, dv))
+    if lse is not None:
+        _contiguous(lse, "lse", torch.float32, (H, B))
+    need = decode_attn_workspace_size(B, H, Hkv, dq, dv) if workspace is None else 0
     workspace, wp, wb = _scratch(workspace, need, q, stream)
-    _check(name, getattr(lib, name)(
-        qp, qs, k_cache.data_ptr(), v_cache.data_ptr(), *scales, block_table.data_ptr(), block_table.shape[1], k_cache.shape[0],
-        ctx, B, H, Hkv, dq, dv, float(softmax_scale), out.data_ptr(), lp, wp, wb, _stream(stream)))
+    _call(name, op, _DECODE_FP8 if scales else _DECODE, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
+          *[s.data_ptr() for s in scales], block_table.data_ptr(), mb, nb, ctx_lens.data_ptr(), B, H, Hkv, dq, dv,
+          softmax_scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(), wp, wb, _stream_ptr(stream, dev))
     return out
 
 
@@ -624,43 +630,40 @@ def vpp_decode_attn(q, k_cache, v_cache, block_table, ctx_lens, out=None, lse=No
     """Attention of one new token per sequence (q [batch, heads, dq]) over a
     bf16 paged cache; ctx_lens (int32 CUDA tensor) is read when the kernel
     runs, and a row of length 0 gives out = 0, lse = -inf."""
-    return _decode_attn("vpp_decode_attn", q, k_cache, v_cache, (), block_table, ctx_lens, out, lse, softmax_scale, workspace,
-                        stream)
+    return _decode_attn("vpp_decode_attn", _OP_DECODE, q, k_cache, v_cache, (), block_table, ctx_lens, out, lse, softmax_scale,
+                        workspace, stream)
 
 
 def vpp_decode_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out=None, lse=None, softmax_scale=0.0,
                         workspace=None, stream=None):
     """vpp_decode_attn over an E4M3 paged cache (uint8 codes, per-kv-head scales)."""
     _scales(k_scale, v_scale, k_cache.shape[2])
-    _on_device(torch.cuda.current_device(), k_scale, v_scale)
-    return _decode_attn("vpp_decode_attn_fp8", q, k_cache, v_cache, (k_scale.data_ptr(), v_scale.data_ptr()), block_table,
-                        ctx_lens, out, lse, softmax_scale, workspace, stream)
+    return _decode_attn("vpp_decode_attn_fp8", _OP_DECODE_FP8, q, k_cache, v_cache, (k_scale, v_scale), block_table, ctx_lens,
+                        out, lse, softmax_scale, workspace, stream)
 
 
-def prompt_attn_workspace_size(batch, total_q, heads, kv_heads):
-    return int(load().vpp_prompt_attn_workspace_size(int(batch), int(total_q), heads, kv_heads))
-
-
-def vpp_prompt_attn(q, k, v, cu_seqlens, out=None, lse=None, softmax_scale=0.0, workspace=None, stream=None):
+def vpp_prompt_attn(q, k, v, cu_seqlens, out=None, lse=None, softmax_scale=0.0, stream=None):
     """Causal attention of whole prompts packed one after the other (q, k, v
     bf16 [tokens, heads, d], contiguous or parts of one fused projection);
     cu_seqlens (int32 CUDA tensor) is read when the kernel runs."""
-    _on_device(torch.cuda.current_device(), q, k, v, cu_seqlens, out, lse, workspace)
+    dev = torch.cuda.current_device()
+    _same_device(dev, q, k, v, cu_seqlens, out, lse)
     T, H, dq = q.shape
-    Hkv, dv = k.shape[1], v.shape[2]
-    qp, qs = _rows(q, "q")
-    kp, ks = _rows(k, "k", Hkv, dq)
-    vp, vs = _rows(v, "v", Hkv, dv)
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v have different token counts")
+    _, Hkv, dv = v.shape
+    qs = _token_stride(q, "q", T, H, dq)
+    ks = _token_stride(k, "k", T, Hkv, dq)
+    vs = _token_stride(v, "v", T, Hkv, dv)
     batch = cu_seqlens.shape[0] - 1
-    cu = _lengths(cu_seqlens, batch + 1, "cu_seqlens")
-    out, lp = _out_lse(out, lse, T, H, dv, q, stream)
-    lib = load()
-    need = lib.vpp_prompt_attn_workspace_size(batch, T, H, Hkv) if workspace is None else 0
-    workspace, wp, wb = _scratch(workspace, need, q, stream)
-    _check("vpp_prompt_attn", lib.vpp_prompt_attn(
-        qp, qs, kp, ks, vp, vs, cu, batch, T, H, Hkv, dq, dv, float(softmax_scale), out.data_ptr(), lp, wp, wb, _stream(stream)))
+    _contiguous(cu_seqlens, "cu_seqlens", torch.int32, (batch + 1,))
+    if out is None:
+        out = _empty((T, H, dv), torch.bfloat16, q, stream)
+    else:
+        _contiguous(out, "out", torch.bfloat16, (T, H, dv))
+    if lse is not None:
+        _contiguous(lse, "lse", torch.float32, (H, T))
+    _call("vpp_prompt_attn", _OP_PROMPT, _PROMPT, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu_seqlens.data_ptr(),
+          batch, T, H, Hkv, dq, dv, softmax_scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+          _stream_ptr(stream, dev))
     return out
 
 

@@ -550,20 +550,31 @@ size_t vpp_decode_attn_workspace_size(int32_t batch, int heads, int kv_heads,
  * 0 .. total_q or ends before it begins is left out and recorded as
  * VPP_ERR_INVALID.
  * out [total_q][heads][head_dim_v] bf16, lse [heads][total_q] float32 (NULL
- * allowed).  workspace: DEVICE, 16-byte aligned,
- * vpp_prompt_attn_workspace_size(...) bytes, holding anything; calls that
- * overlap on the GPU need one each.  total_q == 0 is a no-op.
+ * allowed).  No workspace; total_q == 0 is a no-op.
  */
 int vpp_prompt_attn(const void *q, int64_t q_stride, const void *k,
                     int64_t k_stride, const void *v, int64_t v_stride,
                     const int32_t *cu_seqlens, int32_t batch, int64_t total_q,
                     int heads, int kv_heads, int head_dim_qk, int head_dim_v,
-                    float softmax_scale, void *out, float *lse,
-                    void *workspace, size_t workspace_bytes, void *stream);
+                    float softmax_scale, void *out, float *lse, void *stream);
 
-/* Workspace bytes of vpp_prompt_attn (independent of the lengths). */
-size_t vpp_prompt_attn_workspace_size(int32_t batch, int64_t total_q,
-                                      int heads, int kv_heads);
+/*
+ * One of the calls above with its arguments, in their order, as an array of
+ * 64-bit words: pointers and whole numbers as they are, a float as its 32-bit
+ * pattern in the low half.  For bindings that convert arguments one by one,
+ * which for thirty of them takes longer than the smallest of these kernels.
+ * nargs other than the call's count, or a word that does not fit its argument,
+ * returns VPP_ERR_INVALID.
+ */
+typedef enum {
+    VPP_CALL_ROPE_APPEND = 1,
+    VPP_CALL_ROPE_APPEND_FP8 = 2,
+    VPP_CALL_DECODE_ATTN = 3,
+    VPP_CALL_DECODE_ATTN_FP8 = 4,
+    VPP_CALL_PROMPT_ATTN = 5
+} vpp_call_op;
+
+int vpp_call(int op, const void *args, int nargs);
 
 /*
  * Device status word: synchronises `stream`, stores the first error any

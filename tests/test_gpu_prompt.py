@@ -127,17 +127,15 @@ def test_equals_the_cached_path():
     check_sequences(a, None, q.cpu(), k.cpu(), v.cpu(), cu, d)
 
 
-def test_runs_give_the_same_bits_and_a_dirty_workspace_is_fine():
+def test_runs_give_the_same_bits():
     H, Hkv, d = 8, 2, 128
     lens = [300, 1, 77, 512, 0, 64]
     cu = starts(lens)
     T = int(cu[-1])
     q, k, v = randn((T, H, d), 15).to(DEV), randn((T, Hkv, d), 16).to(DEV), randn((T, Hkv, d), 17).to(DEV)
-    ws = torch.empty(vpp.prompt_attn_workspace_size(len(lens), T, H, Hkv) + 16, dtype=torch.uint8, device=DEV)
     want = vpp.vpp_prompt_attn(q, k, v, cu.to(DEV))
-    for fill in (0, 127, 255):
-        ws.fill_(fill)
-        assert torch.equal(vpp.vpp_prompt_attn(q, k, v, cu.to(DEV), workspace=ws), want)
+    for _ in range(5):
+        assert torch.equal(vpp.vpp_prompt_attn(q, k, v, cu.to(DEV)), want)
 
 
 def test_captured_call_follows_the_lengths():
@@ -146,12 +144,11 @@ def test_captured_call_follows_the_lengths():
     qd, kd, vd = q.to(DEV), k.to(DEV), v.to(DEV)
     cu = torch.zeros(7, dtype=torch.int32, device=DEV)
     out, lse = torch.empty((T, H, d), dtype=torch.bfloat16, device=DEV), torch.empty((H, T), device=DEV)
-    ws = torch.empty(vpp.prompt_attn_workspace_size(6, T, H, Hkv) + 16, dtype=torch.uint8, device=DEV)
-    vpp.vpp_prompt_attn(qd, kd, vd, cu, out=out, lse=lse, workspace=ws)
+    vpp.vpp_prompt_attn(qd, kd, vd, cu, out=out, lse=lse)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        vpp.vpp_prompt_attn(qd, kd, vd, cu, out=out, lse=lse, workspace=ws)
+        vpp.vpp_prompt_attn(qd, kd, vd, cu, out=out, lse=lse)
     for lens in ([900, 0, 0, 0, 0, 0], [100] * 6, [1, 2, 3, 4, 5, 6], [0, 0, 0, 0, 0, 900], [450, 300, 50, 60, 39, 1]):
         now = starts(lens)
         cu.copy_(now)

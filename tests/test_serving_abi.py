@@ -2,6 +2,7 @@
 the host before any launch, so these run without a GPU."""
 
 import ctypes
+import struct
 
 import pytest
 
@@ -22,8 +23,7 @@ ROPE = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, cs=P, rows=64, start=0, rot=6
             kc=P, vc=P, bt=P, mb=4, nb=8, cu=P, ctx=P, batch=2, T=5, H=8, Hkv=4, dq=64, dv=64, st=None)
 DEC = dict(q=P, qs=512, kc=P, vc=P, bt=P, mb=4, nb=8, ctx=P, batch=2, H=8, Hkv=4, dq=64, dv=64, scale=0.0, out=P, lse=P, ws=P, wb=1 << 40,
            st=None)
-PRO = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, cu=P, batch=2, T=5, H=8, Hkv=4, dq=64, dv=64, scale=0.0, out=P, lse=P, ws=P,
-           wb=1 << 40, st=None)
+PRO = dict(q=P, qs=512, k=P, ks=256, v=P, vs=256, cu=P, batch=2, T=5, H=8, Hkv=4, dq=64, dv=64, scale=0.0, out=P, lse=P, st=None)
 
 
 def args(base, change):
@@ -99,13 +99,55 @@ def test_empty_calls_are_no_ops(lib):
     assert lib.vpp_prompt_attn(*args(PRO, dict(T=0, q=None, k=None, v=None, cu=None, out=None, lse=None))) == vpp.VPP_OK
 
 
+def words(values):
+    return b"".join(struct.pack("=f4x", v) if isinstance(v, float) else struct.pack("=q", v or 0) for v in values)
+
+
+CALLS = [(1, ROPE, {}, "vpp_rope_append"), (3, DEC, {}, "vpp_decode_attn"), (5, PRO, {}, "vpp_prompt_attn")]
+
+
+@pytest.mark.parametrize("op,base,_,name", CALLS)
+def test_packed_call_checks_like_the_call(lib, op, base, _, name):
+    """Every argument, spoilt in turn, gives the same answer both ways (without a device, the answer of the good call is
+    the missing device's)."""
+    for key in [None] + list(base):
+        if key == "st":
+            continue
+        for spoilt in (None, 3, -1, BAD):
+            if key is not None and isinstance(base[key], float):
+                continue
+            a = args(base, {} if key is None else {key: spoilt})
+            narrow = key not in (None, "q", "k", "v", "qo", "ko", "kc", "vc", "bt", "cu", "ctx", "out", "lse", "ws", "cs")
+            if spoilt is None and narrow or (spoilt == -1 and not narrow) or (key == "wb"):
+                continue
+            if key is None:
+                a = args(base, dict(Hkv=3))  # refused, so that nothing is launched where there is a device
+            elif spoilt == 3 and key in ("rows", "mb", "nb", "batch", "T", "il"):
+                continue  # a good value: would launch
+            elif key in ("ko", "ctx") and spoilt is None or (key == "lse" and spoilt is None):
+                continue  # may be missing: would launch
+            elif spoilt == BAD and (key == "lse" or key == "ctx" or key == "cu" or key == "bt" or key == "cs" or narrow):
+                continue
+            want = getattr(lib, name)(*a)
+            assert want != vpp.VPP_OK
+            assert lib.vpp_call(op, words(a), len(a)) == want, (key, spoilt)
+
+
+def test_packed_call_refuses_other_counts_and_wide_words(lib):
+    for op, base, _, _name in CALLS:
+        a = args(base, {})
+        assert lib.vpp_call(op, words(a) + bytes(8), len(a) + 1) == INV
+        assert lib.vpp_call(op, words(a), len(a) - 1) == INV
+        assert lib.vpp_call(op, words(args(base, dict(H=8 + (1 << 32)))), len(a)) == INV
+    assert lib.vpp_call(0, words([0] * 40), 29) == INV
+    assert lib.vpp_call(9, words([0] * 40), 29) == INV
+    assert lib.vpp_call(1, None, 29) == INV
+
+
 def test_workspace_sizes(lib):
     assert vpp.decode_attn_workspace_size(0, 8, 2, 128, 128) == 0
     assert vpp.decode_attn_workspace_size(4, 7, 2, 128, 128) == 0
     assert vpp.decode_attn_workspace_size(4, 8, 2, 96, 128) == 0
-    assert vpp.prompt_attn_workspace_size(0, 10, 8, 2) == 0
-    assert vpp.prompt_attn_workspace_size(3, -1, 8, 2) == 0
-    assert vpp.prompt_attn_workspace_size(3, 10, 7, 2) == 0
     assert vpp.decode_attn_workspace_size(1, 8, 2, 128, 128) >= 0
 
 
