@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "fp8.cuh"
+#include "prompt_attn.cuh"
 #include "serve.cuh"
 #include "vpp.h"
 
@@ -1345,23 +1346,20 @@ int vpp_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_st
       make_packed_kv_map(&tm_k, k, k_stride, total_q, kv_heads, head_dim_qk) ||
       make_packed_kv_map(&tm_v, v, v_stride, total_q, kv_heads, head_dim_v))
     return VPP_ERR_INVALID;
-  PackedParams p = {};
-  p.heads = heads;
-  p.kv_heads = kv_heads;
-  p.group = heads / kv_heads;
-  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)head_dim_qk);
-  p.scale_log2 = scale * 1.4426950408889634f;
+  PromptParams p = {};
+  p.cu = cu_seqlens;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  p.lse_stride = total_q;
-  p.status = ds->status;
-  p.cu = cu_seqlens;
-  p.batch = batch;
   p.total = total_q;
-  // At most total / 2T whole pairs and one partial pair per sequence.
-  const int64_t items = total_q / (2 * (kTileM / p.group)) + std::min<int64_t>(batch, total_q);
-  if (items * kv_heads > INT32_MAX) return VPP_ERR_INVALID;
-  return launch_packed_attn(head_dim_qk, head_dim_v, tm_q, tm_k, tm_v, p, (int)(items * kv_heads), as_stream(stream)) ==
+  p.batch = batch;
+  p.heads = heads;
+  p.kv_heads = kv_heads;
+  p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)head_dim_qk)) * 1.4426950408889634f;
+  p.status = ds->status;
+  // At most total / 2T whole pairs of query tiles and one partial pair per sequence.
+  const int64_t items = total_q / (2 * (kTileM / (heads / kv_heads))) + std::min<int64_t>(batch, total_q);
+  if (items * kv_heads > INT32_MAX / 2) return VPP_ERR_INVALID;
+  return launch_prompt_attn(head_dim_qk, head_dim_v, tm_q, tm_k, tm_v, p, items, ds->num_sms, as_stream(stream)) ==
                  cudaSuccess
              ? VPP_OK
              : VPP_ERR_CUDA;

@@ -28,7 +28,7 @@ struct AttnSeg {
   int64_t ws_row0;     // first workspace row of this segment's partials
 };
 
-struct AttnCommon {
+struct AttnParams {
   int32_t n_segs;
   int32_t heads;
   int32_t kv_heads;
@@ -46,17 +46,7 @@ struct AttnCommon {
   const float* k_scale;   // [kv_heads] factor on every key (fp8 cache), may be null
   const float* v_scale;   // [kv_heads] factor on every value (fp8 cache), may be null
   int* status;
-};
-
-struct AttnParams : AttnCommon {
   AttnSeg segs[kMaxAttnSegs];
-};
-
-// Packed prompts: the segments are read on the device from cu_seqlens.
-struct PackedParams : AttnCommon {
-  const int32_t* cu;      // [batch + 1]
-  int32_t batch;
-  int64_t total;          // packed rows
 };
 
 // Smem and thread shape of one instantiation.
@@ -91,11 +81,6 @@ __host__ __device__ constexpr int attn_smem_bytes(int dq, int dv, bool f8 = fals
 cudaError_t launch_chunk_attn(int dq, int dv, bool f8, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                               const CUtensorMap& tm_v, const AttnParams& p, int grid,
                               cudaStream_t stream);
-
-// Causal attention of packed prompts (bf16, contiguous maps whose token
-// stride is the caller's), grid = item bound x kv heads.
-cudaError_t launch_packed_attn(int dq, int dv, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                               const CUtensorMap& tm_v, const PackedParams& p, int grid, cudaStream_t stream);
 
 // Merge of split partials for one segment (a7).
 cudaError_t launch_lse_merge(const float* ws_o, const float* ws_lse, int64_t ws_row0,

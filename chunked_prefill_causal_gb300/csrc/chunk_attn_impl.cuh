@@ -184,98 +184,12 @@ __device__ __forceinline__ void exps_to_tmem(const float (&sv)[128], float2 sl2,
 
 }  // namespace attn_detail
 
-// Packed prompts (PK): the segment and query-tile pair of item i.  Sequence b
-// has np_b = ceil(len_b / 2T) pairs; pair j of any sequence attends to about
-// (j + 1) 2T keys, so the items are ordered by j, largest first, and then by
-// sequence: the heaviest start first, as for the segments planned on the
-// host.  F(j) = sum_b max(0, np_b - j) counts the items of pair index >= j, so
-// the item's j is the largest with F(j) > i, found by bisection, and its
-// sequence is the (i - F(j + 1))-th with np_b > j.  Up to 32 sequences every
-// warp does this by itself (one sequence a lane); with more, the whole CTA.
-// A sequence whose range is not within 0 .. total is left out and reported.
-// Returns false when there is no item i.
-template <int THREADS>
-__device__ __forceinline__ bool packed_item(const PackedParams& p, int item, int T2, int* scratch, AttnSeg* seg,
-                                            int* pair) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool small = p.batch <= 32;
-  const int at0 = small ? lane : tid, step = small ? 32 : THREADS;
-  auto pairs = [&](int b) {
-    if (b >= p.batch) return 0;
-    const int lo = __ldg(p.cu + b), hi = __ldg(p.cu + b + 1);
-    if (lo < 0 || hi < lo || hi > p.total) {
-      if (blockIdx.x == 0) record_status(p.status, kStatusInvalid);
-      return 0;
-    }
-    return static_cast<int>((static_cast<int64_t>(hi) - lo + T2 - 1) / T2);
-  };
-  const int np0 = pairs(at0);
-  // Sum over all sequences of f(np_b); every thread gets it.
-  auto all = [&](auto f) {
-    int s = f(np0);
-    for (int b = at0 + step; b < p.batch; b += step) s += f(pairs(b));
-    s = __reduce_add_sync(0xffffffffu, s);
-    if (!small) {
-      if (lane == 0) scratch[warp] = s;
-      __syncthreads();
-      s = 0;
-#pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) s += scratch[w];
-      __syncthreads();
-    }
-    return s;
-  };
-  int j = 0, hi = static_cast<int>((p.total + T2 - 1) / T2);  // F(j) > item >= F(hi) (F(hi) = 0)
-  if (all([](int n) { return n; }) <= item) return false;
-  while (hi - j > 1) {
-    const int mid = (j + hi) >> 1;
-    if (all([&](int n) { return max(0, n - mid); }) > item) j = mid; else hi = mid;
-  }
-  int rank = item - all([&](int n) { return max(0, n - j - 1); });
-  int b = 0;
-  if (small) {
-    const uint32_t mask = __ballot_sync(0xffffffffu, np0 > j);
-    const bool mine = np0 > j && __popc(mask & ((1u << lane) - 1u)) == rank;
-    b = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-  } else {
-    for (int base = 0;; base += THREADS) {
-      const bool in = (base == 0 ? np0 : pairs(base + tid)) > j;
-      const uint32_t mask = __ballot_sync(0xffffffffu, in);
-      if (lane == 0) scratch[warp] = __popc(mask);
-      __syncthreads();
-      int before = 0, n = 0;
-#pragma unroll
-      for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += scratch[w];
-        n += scratch[w];
-      }
-      if (in && before + __popc(mask & ((1u << lane) - 1u)) == rank) scratch[THREADS / 32] = base + tid;
-      __syncthreads();
-      if (rank < n) break;
-      rank -= n;
-    }
-    b = scratch[THREADS / 32];
-  }
-  const int lo = __ldg(p.cu + b), len = __ldg(p.cu + b + 1) - lo;
-  seg->q_start = lo;
-  seg->q_len = len;
-  seg->kv_len = len;
-  seg->table_off = 0;
-  seg->n_splits = 1;
-  seg->split_keys = 0;
-  seg->kv_base = lo;
-  seg->ws_row0 = 0;
-  *pair = j;
-  return true;
-}
-
-template <int DQ, int DV, bool F8, bool PK = false>
+template <int DQ, int DV, bool F8>
 __global__ void __launch_bounds__(attn_threads(F8), 1)
     chunk_attn_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v,
-                      const __grid_constant__ std::conditional_t<PK, PackedParams, AttnParams> p) {
-  static_assert(!(F8 && PK), "packed prompts are bf16");
+                      const __grid_constant__ AttnParams p) {
   using namespace attn_detail;
   using S = Shape<DQ, DV, F8>;
   extern __shared__ uint8_t smem_raw[];
@@ -294,31 +208,19 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
   const int lane = threadIdx.x & 31;
 
   // ---------------------------------------------------------- work item
+  int si = 0;
+  while (si + 1 < p.n_segs && p.segs[si + 1].cta_begin <= static_cast<int>(blockIdx.x)) ++si;
+  const AttnSeg& seg = p.segs[si];
+  const int local = static_cast<int>(blockIdx.x) - seg.cta_begin;
+  // CTA order: key range fastest, then query-tile pairs (heaviest first), then
+  // kv head, so the CTAs resident at one time read the same kv head's K/V
+  // tiles and share them through L2.
+  const int split = local % seg.n_splits;
+  const int rest = local / seg.n_splits;
+  const int pair = seg.n_pairs - 1 - rest % seg.n_pairs;
+  const int g = rest / seg.n_pairs;
   const int G = p.group;
   const int T = kTileM / G;       // tokens per query tile
-  AttnSeg packed_seg;
-  const AttnSeg* seg_p = &packed_seg;
-  int split = 0, pair, g;
-  if constexpr (PK) {
-    const int item = static_cast<int>(blockIdx.x) / p.kv_heads;
-    g = static_cast<int>(blockIdx.x) - item * p.kv_heads;
-    // (the ring is scratch before the first copy into it)
-    if (!packed_item<attn_threads(F8)>(p, item, 2 * T, reinterpret_cast<int*>(sRing), &packed_seg, &pair)) return;
-    fence_proxy_async_smem();
-  } else {
-    int si = 0;
-    while (si + 1 < p.n_segs && p.segs[si + 1].cta_begin <= static_cast<int>(blockIdx.x)) ++si;
-    seg_p = &p.segs[si];
-    const int local = static_cast<int>(blockIdx.x) - seg_p->cta_begin;
-    // CTA order: key range fastest, then query-tile pairs (heaviest first), then
-    // kv head, so the CTAs resident at one time read the same kv head's K/V
-    // tiles and share them through L2.
-    split = local % seg_p->n_splits;
-    const int rest = local / seg_p->n_splits;
-    pair = seg_p->n_pairs - 1 - rest % seg_p->n_pairs;
-    g = rest / seg_p->n_pairs;
-  }
-  const AttnSeg& seg = *seg_p;
   const int tok0 = pair * 2 * T;  // first token of tile A (segment-relative)
   const int P = seg.kv_len - seg.q_len;
   const int k_lo = split * seg.split_keys;
@@ -406,9 +308,7 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
-      // (packed prompts: a group that does not divide 128 leaves the last rows
-      // of a tile unused)
-      mbar_arrive_expect_tx(bar(S::B_Q), 2 * S::NQC * (PK ? G * T * 128 : kSubTileBytes));
+      mbar_arrive_expect_tx(bar(S::B_Q), 2 * S::NQC * kSubTileBytes);
       for (int x = 0; x < 2; ++x)
         for (int c = 0; c < S::NQC; ++c)
           tma_load_4d(smem_u32(sQ + (x * S::NQC + c) * kSubTileBytes), &tm_q, bar(S::B_Q),
@@ -429,7 +329,7 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
       auto load_tile = [&](const CUtensorMap* m, int nsub, int pos, uint32_t fb, int c0, int c1) {
         for (int c = 0; c < nsub; ++c) {
           const uint32_t d = smem_u32(sRing + ((pos + c) % S::NSLOT) * kSubTileBytes);
-          if (!PK && p.paged) {
+          if (p.paged) {
             tma_load_4d(d, m, fb, c * 64, g, 0, c0);
             tma_load_4d(d + kSubTileBytes / 2, m, fb, c * 64, g, 0, c1);
           } else {
@@ -441,7 +341,7 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
       for (int j = 0; ok && j < n_kv; ++j) {
         const int key0 = k_lo + j * kTileN;
         int c0, c1;
-        if (!PK && p.paged) {
+        if (p.paged) {
           c0 = block_coord(key0 / kBlockTokens);
           c1 = block_coord(key0 / kBlockTokens + 1);
         } else {
@@ -468,14 +368,9 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
           // the pool holds there; their V rows are zeroed before the tile is
           // released so that P = 0 times them stays 0 (K rows there are masked
           // to -inf before the softmax).  This happens at most once per CTA.
-          // (Packed prompts: these are other sequences' rows, up to a whole tile of
-          // them, in the last tile of many CTAs; warp 2 zeroes them.)
           const int r0 = seg.kv_len - key0;
-          const bool fix = part == 1 && (PK || p.paged) && r0 > 0 && r0 < kTileN && (PK || (r0 % kBlockTokens) != 0);
-          if (PK && fix) {
-            mbar_arrive_expect_tx(bar(S::B_TMP), nsub * kSubTileBytes);
-            load_tile(m, nsub, pos, bar(S::B_TMP), c0, c1);
-          } else if (!fix) {
+          const bool fix = part == 1 && p.paged && r0 > 0 && r0 < kTileN && (r0 % kBlockTokens) != 0;
+          if (!fix) {
             mbar_arrive_expect_tx(fb, nsub * kSubTileBytes);
             load_tile(m, nsub, pos, fb, c0, c1);
           } else {
@@ -506,23 +401,6 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
         for (int t = issued > S::NB ? issued - S::NB : 0; t < issued; ++t)
           mbar_wait_for(bar(S::B_FULL + t % S::NB), (t / S::NB) & 1u, kCleanupNs);
         mbar_wait_for(bar(S::B_Q), 0, kCleanupNs);
-        if (PK && issued == 2 * n_kv) mbar_wait_for(bar(S::B_TMP), 0, kCleanupNs);
-      }
-    } else if (PK && warp == 2) {
-      // ------------------------- V rows past the sequence in its last tile
-      const int r0 = seg.kv_len - (n_kv - 1) * kTileN;
-      if (r0 < kTileN && warp_wait(bar(S::B_TMP), 0, p.status, abort_flag)) {
-        const int t = 2 * n_kv - 1;
-        const int pos = S::tile_pos(t);
-        // rows r0 .. 127 of each sub-tile, 128 bytes a row
-        for (int i = r0 * 8 + lane; i < kTileN * 8; i += 32)
-#pragma unroll
-          for (int c = 0; c < S::NVC; ++c)
-            *reinterpret_cast<uint4*>(sRing + ((pos + c) % S::NSLOT) * kSubTileBytes + i * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(S::B_FULL + t % S::NB));
       }
     } else if ((warp == 1 || warp == 3) && lane == 0) {
       // ---------------------------------------------------- MMA issuer
@@ -878,10 +756,10 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
     if (ok) ok = warp_wait(bar(S::B_O + x), 0, p.status, abort_flag);
     if (ok) {
       tc_fence_after();
-      const bool valid = tok < seg.q_len && (!PK || row < G * T);
+      const bool valid = tok < seg.q_len;
       const float inv = vsc / l;
       const float lse_v = m * kLn2 + logf(l);
-      if (PK || seg.n_splits == 1) {
+      if (seg.n_splits == 1) {
         uint16_t* orow = p.out + (static_cast<int64_t>(seg.q_start + tok) * p.heads + hq) * DV;
 #pragma unroll
         for (int q = 0; q < DV / 32; ++q) {
@@ -944,23 +822,6 @@ __global__ void __launch_bounds__(attn_threads(F8), 1)
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
-}
-
-template <int DQ, int DV>
-cudaError_t launch_packed_attn_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                 const PackedParams& p, int grid, cudaStream_t stream) {
-  constexpr int smem = attn_smem_bytes(DQ, DV, false);
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  static bool configured[64] = {};
-  if (dev < 64 && !configured[dev]) {
-    e = cudaFuncSetAttribute(chunk_attn_kernel<DQ, DV, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
-  chunk_attn_kernel<DQ, DV, false, true><<<grid, attn_threads(false), smem, stream>>>(tm_q, tm_k, tm_v, p);
-  return cudaGetLastError();
 }
 
 template <int DQ, int DV, bool F8>

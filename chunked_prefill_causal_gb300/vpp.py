@@ -12,6 +12,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 
 import torch
 
@@ -487,6 +488,8 @@ def _token_stride(t, what, n, h, d):
     projection is); the stride of a single token is never used and reported as the row's length."""
     if t.dtype is not torch.bfloat16 or t.shape != (n, h, d):
         raise ValueError(f"{what} must be bf16 {[n, h, d]}, not {t.dtype} {list(t.shape)}")
+    if t.is_contiguous():
+        return h * d
     st, sh, sd = t.stride()
     if (sd != 1 and d > 1) or (sh != d and h > 1):
         raise ValueError(f"{what}: a token's heads must be contiguous")
@@ -517,12 +520,31 @@ def _empty(shape, dtype, like, stream):
     return t
 
 
-def _scratch(workspace, need, like, stream):
-    """(tensor, pointer, bytes) of the caller's workspace, or of one allocated for this call."""
+class _Scratch(threading.local):
+    """The workspaces of one thread, by device and stream.  Calls of a thread on a stream run one after the other, so they
+    can share one; a captured call may be replayed beside them, and another thread may call between a call's two kernels,
+    so those get their own."""
+
+    def __init__(self):
+        self.by_stream = {}
+
+
+_scratches = _Scratch()
+
+
+def _scratch(workspace, need, like, stream, dev, raw):
+    """(tensor, pointer, bytes) of the caller's workspace, or of one of at least `need` bytes for this call."""
     if workspace is None:
         if need == 0:
             return None, 0, 0
-        workspace = _empty(need, torch.uint8, like, stream)
+        if stream is not None or torch.cuda.is_current_stream_capturing():
+            workspace = _empty(need, torch.uint8, like, stream)
+        else:
+            kept = _scratches.by_stream.get((dev, raw))
+            if kept is None or kept[2] < need:
+                t = torch.empty(need, dtype=torch.uint8, device=like.device)
+                kept = _scratches.by_stream[(dev, raw)] = (t, t.data_ptr(), need)
+            return kept
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -617,11 +639,12 @@ def _decode_attn(name, op, q, k_cache, v_cache, scales, block_table, ctx_lens, o
         _contiguous(out, "out", torch.bfloat16, (B, H, dv))
     if lse is not None:
         _contiguous(lse, "lse", torch.float32, (H, B))
+    raw = _stream_ptr(stream, dev)
     need = decode_attn_workspace_size(B, H, Hkv, dq, dv) if workspace is None else 0
-    workspace, wp, wb = _scratch(workspace, need, q, stream)
+    workspace, wp, wb = _scratch(workspace, need, q, stream, dev, raw)
     _call(name, op, _DECODE_FP8 if scales else _DECODE, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
           *[s.data_ptr() for s in scales], block_table.data_ptr(), mb, nb, ctx_lens.data_ptr(), B, H, Hkv, dq, dv,
-          softmax_scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(), wp, wb, _stream_ptr(stream, dev))
+          softmax_scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(), wp, wb, raw)
     return out
 
 
@@ -629,7 +652,9 @@ def vpp_decode_attn(q, k_cache, v_cache, block_table, ctx_lens, out=None, lse=No
                     stream=None):
     """Attention of one new token per sequence (q [batch, heads, dq]) over a
     bf16 paged cache; ctx_lens (int32 CUDA tensor) is read when the kernel
-    runs, and a row of length 0 gives out = 0, lse = -inf."""
+    runs, and a row of length 0 gives out = 0, lse = -inf.  Without a
+    workspace the calls of a thread on the current stream share one; calls
+    under capture or on a given stream allocate their own."""
     return _decode_attn("vpp_decode_attn", _OP_DECODE, q, k_cache, v_cache, (), block_table, ctx_lens, out, lse, softmax_scale,
                         workspace, stream)
 
