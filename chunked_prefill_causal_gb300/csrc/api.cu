@@ -1356,11 +1356,9 @@ int vpp_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_st
   p.kv_heads = kv_heads;
   p.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)head_dim_qk)) * 1.4426950408889634f;
   p.status = ds->status;
-  // At most total / 2T whole pairs of query tiles and one partial pair per sequence.
-  const int64_t items = total_q / (2 * (kTileM / (heads / kv_heads))) + std::min<int64_t>(batch, total_q);
-  if (items * kv_heads > INT32_MAX / 2) return VPP_ERR_INVALID;
-  return launch_prompt_attn(head_dim_qk, head_dim_v, tm_q, tm_k, tm_v, p, items, ds->num_sms, as_stream(stream)) ==
-                 cudaSuccess
+  // (one item per tile or sequence and kv head, counted in 32 bits)
+  if ((total_q / 8 + std::min<int64_t>(batch, total_q) + 1) * kv_heads > INT32_MAX / 2) return VPP_ERR_INVALID;
+  return launch_prompt_attn(head_dim_qk, head_dim_v, tm_q, tm_k, tm_v, p, ds->num_sms, as_stream(stream)) == cudaSuccess
              ? VPP_OK
              : VPP_ERR_CUDA;
 }

@@ -9,20 +9,21 @@
 // 128-row query tiles per CTA take turns on the tensor core, each row of a tile
 // is one softmax thread, P is read from TMEM by the P V product.  Around it:
 //
-// Items.  An item is a pair of query tiles (2T tokens, T = floor(128 / G), times the G
-// heads of one kv head) of one sequence.  The sequences are read from
-// cu_seqlens on the device.  Sequence b has np_b = ceil(len_b / 2T) pairs, and pair j
-// attends to about (j + 1) 2T keys whatever its sequence, so the items are
-// ordered by j, largest first: F(j) = sum_b max(0, np_b - j) counts those of
-// pair index >= j; item i has the largest j with F(j) > i, found by bisection, and
-// belongs to the (i - F(j + 1))-th sequence with np_b > j.
+// Items.  An item is one or two query tiles (T = floor(128 / G) tokens of the G heads of
+// one kv head each) of one sequence, and the grid has a CTA for each.  The
+// sequences are read from cu_seqlens on the device; they are ordered by length
+// class, longest first, and a sequence's items from its last tokens to its first,
+// head by head: the heaviest start first, and the items that read the same keys
+// and values run at the same time.  (Ordered by their weight alone, equal prompts
+// read each key from HBM once per tile of queries: 32768 tokens in prompts of
+// 512 moved 1.25 GB for the 0.4 GB that there are.)
 //
-// Persistent CTAs.  One CTA per SM takes every grid-th item, the order
-// reversed in every other round, which evens out the rounds' sums.  The chunk
-// kernel's one-item CTAs cost about 8 us each besides their keys (launch, TMEM, first
-// loads, drain, output), most of the time of short prompts.  Here the next item's
-// Q and K/V copies and its first Q K^T run while the last softmax and the output
-// of the current one do.
+// Persistent CTAs.  A resident CTA takes over the grid's next one that has not
+// started (cluster launch control), so the items go to whichever SM is free, in
+// order, without a counter in memory.  The chunk kernel's one-item CTAs cost
+// about 8 us each besides their keys (launch, TMEM, first loads, drain, output),
+// most of the time of short prompts; here the next item's Q and K/V copies and its
+// first Q K^T run while the last softmax and the output of the current one do.
 //
 //   warp 0      TMA producer (Q of the item, then K and V tiles, ring of 16 KB slots)
 //   warp 1, 3   MMA issuers of query tiles A and B, taking turns
@@ -37,6 +38,7 @@
 //
 // Bound by the tensor core for long prompts, by the chain of one item for short ones.
 #include <algorithm>
+#include <climits>
 
 #include "chunk_attn_impl.cuh"
 #include "prompt_attn.cuh"
@@ -56,77 +58,194 @@ struct Item {
   int pad[2];
 };
 
-template <int DQ, int DV>
-struct PShape : Shape<DQ, DV, false> {
+// PAIR: two query tiles a CTA, one CTA per SM.  Otherwise one tile, two CTAs.
+template <int DQ, int DV, bool PAIR>
+struct PShape {
   using S = Shape<DQ, DV, false>;
+  static constexpr int TILES = PAIR ? 2 : 1;
+  static constexpr int CTAS = PAIR ? 1 : 2;  // per SM
+  static constexpr int NQC = S::NQC, NVC = S::NVC;
+  static constexpr int QBYTES = TILES * NQC * kSubTileBytes;
+  static constexpr int SOFTMAX = 128 * TILES;
+  static constexpr int THREADS = 128 + SOFTMAX;
+  // 228 KB per SM, 1 KB of it per CTA for the system; 640 bytes for the
+  // entries and barriers.
+  static constexpr int LIMIT = 228 * 1024 / CTAS - 1024;
+  static constexpr int FIT = (LIMIT - QBYTES - 640) / kSubTileBytes;
+  static constexpr int NSLOT = FIT > 12 ? 12 : FIT;
+  static constexpr int NB = NSLOT;
+  static_assert(NSLOT >= NQC + NVC, "ring must hold one K and one V tile");
+  static constexpr int REGS_LOW = PAIR ? kRegsLow : 48;
+  static constexpr int REGS_HIGH = PAIR ? kRegsHigh : 208;
+  static_assert(128 * REGS_LOW + SOFTMAX * REGS_HIGH <= THREADS * (PAIR ? 168 : 128), "register split exceeds the launch");
+  static constexpr int TMEM_COLS = 256 * TILES;  // S tiles, then O tiles
+  static constexpr int PV0 = S::PV0, KP0 = S::KP0;
+  static constexpr bool SPLIT_P = S::SPLIT_P, EARLY_V = S::EARLY_V;
   static constexpr int B_Q = 0, B_QE = 1, B_S = 2, B_P = 4, B_P1 = 6, B_O = 8, B_FINAL = 10, B_END = 12, B_IF = 13,
-                       B_IE = B_IF + kEntries, B_FULL = B_IE + kEntries, B_EMPTY = B_FULL + S::NB,
-                       B_TMP = B_EMPTY + S::NB, NBARS = B_TMP + S::NB;
-  static constexpr int SMEM = 1024 + S::QBYTES + S::NSLOT * kSubTileBytes + kEntries * 32 + NBARS * 8 + 16;
-  static_assert(SMEM <= kSmemLimit, "shared memory budget");
+                       B_IE = B_IF + kEntries, B_FULL = B_IE + kEntries, B_EMPTY = B_FULL + NB, B_TMP = B_EMPTY + NB,
+                       B_CLC = B_TMP + NB, NBARS = B_CLC + 1;
+  static constexpr int SMEM = QBYTES + NSLOT * kSubTileBytes + (kEntries + 1) * 32 + NBARS * 8 + 16;
+  static_assert(SMEM <= LIMIT && SMEM <= kSmemLimit, "shared memory budget");
+  // Tile t of the load order (K_0, V_0, K_1, ...): first ring position and slots.
+  __device__ __forceinline__ static int tile_pos(int t) { return S::tile_pos(t); }
+  __device__ __forceinline__ static int tile_slots(int t) { return S::tile_slots(t); }
 };
 
-// The work list, by one warp: a sequence per lane, more in further rounds.
+// The work list, by one warp.  The first kHeld x 32 sequences' item counts stay
+// in registers (a sequence per lane and register), those of further ones are
+// read again in each pass.  Items are asked for in increasing order, so a scan
+// goes on where the one before left it.
 struct Finder {
+  static constexpr int kHeld = 8;
   const PromptParams& p;
-  int T2, lane, np0, hi;  // hi: F(hi) <= every item still to come
-  __device__ __forceinline__ Finder(const PromptParams& p_, int T2_) : p(p_), T2(T2_) {
+  int tokens, lane;     // tokens of an item
+  int np[kHeld];
+  int lo, hi;           // the class: sequences with lo <= np < hi
+  int before, items;    // items of the classes before, and of this one
+  int scan_base, scan;  // sequences scanned in this class, and their items
+  int np_b;             // np of the sequence found
+  int pair;             // index of the item in it
+  __device__ __forceinline__ Finder(const PromptParams& p_, int tokens_) : p(p_), tokens(tokens_) {
     lane = threadIdx.x & 31;
-    np0 = pairs(lane);
-    hi = static_cast<int>((p.total + T2 - 1) / T2);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) np[k] = pairs(32 * k + lane);
+    lo = hi = INT_MAX;
+    before = items = scan_base = scan = 0;
   }
   __device__ __forceinline__ int pairs(int b) const {
     if (b >= p.batch) return 0;
-    const int lo = __ldg(p.cu + b), end = __ldg(p.cu + b + 1);
-    if (lo < 0 || end < lo || end > p.total) {
+    const int start = __ldg(p.cu + b), end = __ldg(p.cu + b + 1);
+    if (start < 0 || end < start || end > p.total) {
       if (blockIdx.x == 0) record_status(p.status, kStatusInvalid);
       return 0;
     }
-    return (end - lo + T2 - 1) / T2;
+    return (end - start + tokens - 1) / tokens;
   }
-  // F(j): pairs of index >= j over all sequences.
-  __device__ __forceinline__ int count(int j) const {
-    int s = max(0, np0 - j);
-    for (int b = lane + 32; b < p.batch; b += 32) s += max(0, pairs(b) - j);
-    return __reduce_add_sync(0xffffffffu, s);
+  // np of sequence base + lane (base a multiple of 32).
+  __device__ __forceinline__ int held(int base) const {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (base == 32 * k) n = np[k];
+    return base >= 32 * kHeld ? pairs(base + lane) : n;
   }
-  // Item i (items are asked for in increasing order, so j only falls).
-  __device__ __forceinline__ void find(int i, int* b_out, int* j_out) {
-    int j = 0, top = hi;  // F(j) > i >= F(top)
-    while (top - j > 1) {
-      const int mid = (j + top) >> 1;
-      if (count(mid) > i) j = mid; else top = mid;
-    }
-    hi = top;
-    int rank = i - count(j + 1);
-    *b_out = -1;  // (none: only when the ranges overlap and the counts overflow)
-    for (int base = 0; base < p.batch; base += 32) {
-      const bool in = (base == 0 ? np0 : pairs(base + lane)) > j;
-      const uint32_t mask = __ballot_sync(0xffffffffu, in);
-      const int n = __popc(mask);
-      if (rank < n) {
-        const bool mine = in && __popc(mask & ((1u << lane) - 1u)) == rank;
-        *b_out = base + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-        *j_out = j;
-        return;
+  // The sequence of item i, or -1 past the last one.
+  __device__ __forceinline__ int find(int i) {
+    while (i >= before + items) {
+      // the next class: the longest sequences left, down to 3/4 of their length
+      before += items;
+      hi = lo;
+      int top = 0;
+#pragma unroll 4
+      for (int base = 0; base < p.batch; base += 32) {
+        const int n = held(base);
+        if (n < hi) top = max(top, n);
       }
-      rank -= n;
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (top == 0) {
+        items = 0;
+        lo = 0;
+        return -1;
+      }
+      lo = top - top / 4;
+      int sum = 0;
+#pragma unroll 4
+      for (int base = 0; base < p.batch; base += 32) {
+        const int n = held(base);
+        if (n >= lo && n < hi) sum += n;
+      }
+      items = __reduce_add_sync(0xffffffffu, sum);
+      scan_base = scan = 0;
     }
+    const int want = i - before;  // among the class's items
+    for (; scan_base < p.batch; scan_base += 32) {
+      int n = held(scan_base);
+      if (n < lo || n >= hi) n = 0;
+      int inc = n;  // inclusive prefix over the lanes
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, want < scan + inc);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        np_b = __shfl_sync(0xffffffffu, n, l);
+        // longest first within the sequence
+        pair = np_b - 1 - (want - (scan + __shfl_sync(0xffffffffu, inc, l) - np_b));
+        return scan_base + l;
+      }
+      scan += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    return -1;  // (only when the ranges overlap so that the counts overflow)
   }
 };
 
-template <int DQ, int DV>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+// Asks the hardware for the next CTA of this grid that has not started, to be
+// run here in its place; the answer (16 bytes) arrives on the mbarrier.
+__device__ __forceinline__ void clc_request(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(bar)
+               : "memory");
+}
+
+// Index of the CTA that was given, -1 when all have started.
+__device__ __forceinline__ int clc_answer(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 a, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, a;\n\t}"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
+}
+
+// w[i] of lane a (of each group of four) becomes w[a] of lane i.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4][4], int a) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit *= 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, (a & bit) ? w[i][c] : w[i | bit][c], bit);
+        if (a & bit) w[i][c] = got; else w[i | bit][c] = got;
+      }
+    }
+  }
+}
+
+// Scores of 32 keys of this thread's row; those past `lim` leave the softmax.
+__device__ __forceinline__ void load_scores(uint32_t taddr, int key, int lim, float (&s)[32]) {
+  uint32_t u[32];
+  tmem_ld32(taddr, u);
+  tmem_ld_wait();
+#pragma unroll
+  for (int k = 0; k < 32; ++k) s[k] = __uint_as_float(u[k]);
+  if (__any_sync(0xffffffffu, key + 31 > lim)) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (key + k > lim) s[k] = -INFINITY;
+  }
+}
+
+template <int DQ, int DV, bool PAIR>
+__global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, PAIR>::CTAS)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PromptParams p) {
-  using S = PShape<DQ, DV>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  using S = PShape<DQ, DV, PAIR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sRing = smem + S::QBYTES;
   Item* entries = reinterpret_cast<Item*>(sRing + S::NSLOT * kSubTileBytes);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(entries + kEntries);
+  uint8_t* clc = reinterpret_cast<uint8_t*>(entries + kEntries);  // 16 bytes
+  uint64_t* bars = reinterpret_cast<uint64_t*>(clc + 32);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::NBARS);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
   volatile int* turn = reinterpret_cast<volatile int*>(tmem_slot + 2);
@@ -141,7 +260,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     *abort_flag = 0u;
     *turn = 0;
     mbar_init(bar(S::B_Q), 1);
-    mbar_init(bar(S::B_QE), 2);
+    mbar_init(bar(S::B_CLC), 1);
+    mbar_init(bar(S::B_QE), S::TILES);
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(S::B_S + x), 1);
       mbar_init(bar(S::B_P + x), 128);
@@ -149,20 +269,20 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_init(bar(S::B_O + x), 1);
       mbar_init(bar(S::B_FINAL + x), 1);
     }
-    mbar_init(bar(S::B_END), 10);  // the 8 softmax warps and the 2 MMA issuers
+    mbar_init(bar(S::B_END), 5 * S::TILES);  // the softmax warps and the MMA issuers
     for (int i = 0; i < kEntries; ++i) {
       mbar_init(bar(S::B_IF + i), 1);
-      mbar_init(bar(S::B_IE + i), 11);  // producer, 2 issuers, 8 softmax warps
+      mbar_init(bar(S::B_IE + i), 1 + 5 * S::TILES);  // producer, issuers, softmax warps
     }
     for (int i = 0; i < S::NB; ++i) {
       mbar_init(bar(S::B_FULL + i), 1);
-      mbar_init(bar(S::B_EMPTY + i), 2);  // released by both MMA issuers
+      mbar_init(bar(S::B_EMPTY + i), S::TILES);  // released by the MMA issuers
       mbar_init(bar(S::B_TMP + i), 1);
     }
     fence_mbar_init();
   }
   if (warp == 2) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -179,7 +299,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   };
 
   if (warp < 4) {
-    regs_dec<kRegsLow>();
+    regs_dec<S::REGS_LOW>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer
       tma_prefetch_desc(&tm_q);
@@ -250,33 +370,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     } else if (warp == 2) {
       // --------------------------------------- items, and V rows of other sequences
-      Finder finder(p, 2 * T);
-      const int total =
-          static_cast<int>(min(static_cast<int64_t>(INT32_MAX / 2), static_cast<int64_t>(finder.count(0)) * p.kv_heads));
-      int round = 0, published = 0;
-      bool done = false, ok = true;
-      auto publish = [&]() {
-        if (done || !ok) return;
-        const int grid = gridDim.x, c = blockIdx.x;
-        int idx = round * grid + ((round & 1) ? grid - 1 - c : c);
-        if (idx >= total) {  // nothing for this CTA in the last round, or past it
-          done = true;
+      Finder finder(p, S::TILES * T);
+      int published = 0, requests = 0;
+      bool ok = true;
+      int idx = blockIdx.x;  // CTA whose item is handed out next, -1: none left
+      auto next_idx = [&]() {
+        __syncwarp();
+        if (lane == 0) {
+          fence_proxy_async_smem();  // after the reads of the answer before
+          mbar_arrive_expect_tx(bar(S::B_CLC), 16);
+          clc_request(smem_u32(clc), bar(S::B_CLC));
         }
-        ++round;
+        ok = warp_wait(bar(S::B_CLC), requests & 1, p.status, abort_flag);
+        if (!ok) mbar_wait_for(bar(S::B_CLC), requests & 1, kCleanupNs);  // lands before the CTA exits
+        ++requests;
+        idx = ok ? clc_answer(smem_u32(clc)) : -1;
+      };
+      auto publish = [&]() {
         Item it{0, 0, 0, 0, 0, 0, {0, 0}};
-        if (!done) {
-          int b, j;
-          const int item = idx / p.kv_heads;
-          finder.find(item, &b, &j);
-          done = b < 0;
-          b = max(b, 0);
+        const int item = idx / p.kv_heads;
+        const int b = idx < 0 ? -1 : finder.find(item);
+        if (b >= 0) {
           it.start = __ldg(p.cu + b);
           it.len = __ldg(p.cu + b + 1) - it.start;
-          it.tok0 = j * 2 * T;
+          it.tok0 = finder.pair * S::TILES * T;
           it.g = idx - item * p.kv_heads;
           it.na = (min(it.tok0 + T, it.len) + kTileN - 1) / kTileN;
-          if (done) it.len = 0;
-          it.nb = it.tok0 + T < it.len ? (min(it.tok0 + 2 * T, it.len) + kTileN - 1) / kTileN : 0;
+          it.nb = PAIR && it.tok0 + T < it.len ? (min(it.tok0 + 2 * T, it.len) + kTileN - 1) / kTileN : 0;
         }
         const int e = published % kEntries;
         if (published >= kEntries &&
@@ -290,14 +410,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         ++published;
       };
       publish();
-      publish();
       int base = 0;
       uint32_t tmp_phase = 0u;
       for (int i = 0; ok; ++i) {
-        publish();  // item i + 2
-        if (!ok || i >= published) break;
         const Item it = entries[i % kEntries];  // (overwritten by item i + 4 at the earliest)
         if (it.len == 0) break;
+        // item i + 1
+        next_idx();
+        if (ok) publish();
+        if (!ok) break;
         const int n = max(it.na, it.nb);
         const int t = 2 * (base + n) - 1;
         const int r0 = it.len - (n - 1) * kTileN;
@@ -317,7 +438,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         base += n;
       }
-    } else if ((warp == 1 || warp == 3) && lane == 0) {
+      // Past the last item the grid has only empty ones (its size is an upper
+      // bound): they are taken here until none is left.
+      while (ok && idx >= 0) next_idx();
+    } else if ((warp == 1 || (PAIR && warp == 3)) && lane == 0) {
       // ---------------------------------------------------- MMA issuer
       const int x = warp == 1 ? 0 : 1;
       const uint64_t dq0 = sdesc_sw128(smem_u32(sQ + x * S::NQC * kSubTileBytes), 16, 1024);
@@ -325,7 +449,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint64_t dv0 = sdesc_sw128(smem_u32(sRing), kSubTileBytes, 1024);  // MN-major
       constexpr uint32_t kSub16 = kSubTileBytes >> 4;
       const uint32_t tS = tbase + x * kTileN;
-      const uint32_t tO = tbase + 2 * kTileN + x * DV;
+      const uint32_t tO = tbase + S::TILES * kTileN + x * DV;
       bool ok = true;
       int base = 0;    // tile pairs of the items before
       int mine = 0;    // S tiles of this query tile before
@@ -359,9 +483,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (j < nx &&
                 !(ok = mbar_wait(bar(S::B_FULL + tk % S::NB), (tk / S::NB) & 1u, p.status, abort_flag)))
               break;
-            // Take the turn: a tight spin on the shared counter (the abort flag
+            // Take the partner's turn: a tight spin on the shared counter (the abort flag
             // and the time limit are checked every 256 polls).
-            if (*turn != my_turn) {
+            if (PAIR && *turn != my_turn) {
               const uint64_t t0 = globaltimer_ns();
               for (uint32_t k = 1; *turn != my_turn; ++k) {
                 if ((k & 255u) != 0) continue;
@@ -382,14 +506,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                   const uint64_t vb = dv0 + vslot * kSub16;
 #pragma unroll
                   for (int k = k0; k < k1; ++k)
-                    umma_ts(tO, tS + 8 * k, vb + k * (2048 >> 4), S::IDESC_PV, (j > 1 || k > 0) ? 1u : 0u);
+                    umma_ts(tO, tS + 8 * k, vb + k * (2048 >> 4), S::S::IDESC_PV, (j > 1 || k > 0) ? 1u : 0u);
                 } else {
 #pragma unroll
                   for (int k = k0; k < k1; ++k)
 #pragma unroll
                     for (int h = 0; h < S::NVC; ++h) {
                       const int vs = vslot + h < S::NSLOT ? vslot + h : vslot + h - S::NSLOT;
-                      umma_ts(tO + 64 * h, tS + 8 * k, dv0 + vs * kSub16 + k * (2048 >> 4), S::IDESC_PV64,
+                      umma_ts(tO + 64 * h, tS + 8 * k, dv0 + vs * kSub16 + k * (2048 >> 4), S::S::IDESC_PV64,
                               (j > 1 || k > 0) ? 1u : 0u);
                     }
                 }
@@ -411,23 +535,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const uint64_t kb = dk0 + ks * kSub16;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  if (c == S::NQC - 1 && k == 0) *turn = my_turn + 1;
-                  umma_ss(tS, dq0 + c * kSub16 + 2 * k, kb + 2 * k, S::IDESC_QK, (c | k) ? 1u : 0u);
+                  if (PAIR && c == S::NQC - 1 && k == 0) *turn = my_turn + 1;
+                  umma_ss(tS, dq0 + c * kSub16 + 2 * k, kb + 2 * k, S::S::IDESC_QK, (c | k) ? 1u : 0u);
                 }
               }
               umma_commit(bar(S::B_S + x));
               umma_commit(bar(S::B_EMPTY + tk % S::NB));
-              if (j >= ny) mbar_arrive(bar(S::B_EMPTY + tk % S::NB));  // the partner does not read this tile
+              if (PAIR && j >= ny) mbar_arrive(bar(S::B_EMPTY + tk % S::NB));  // the partner does not read this tile
               if (j == nx - 1) {
                 umma_commit(bar(S::B_QE));
-                if (ny == 0) mbar_arrive(bar(S::B_QE));
+                if (PAIR && ny == 0) mbar_arrive(bar(S::B_QE));
               }
-            } else {
+            } else if (PAIR) {
               *turn = my_turn + 1;
             }
             if (j > 0) {
               if (!S::EARLY_V) umma_commit(bar(S::B_EMPTY + tv % S::NB));
-              if (j - 1 >= ny) mbar_arrive(bar(S::B_EMPTY + tv % S::NB));
+              if (PAIR && j - 1 >= ny) mbar_arrive(bar(S::B_EMPTY + tv % S::NB));
             }
             if (j == nx) umma_commit(bar(S::B_O + x));
           }
@@ -452,7 +576,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int row_tok = row / G, row_head = row % G;
     const uint32_t lane_base = tbase + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t tS = lane_base + x * kTileN;
-    const uint32_t tO = lane_base + 2 * kTileN + x * DV;
+    const uint32_t tO = lane_base + S::TILES * kTileN + x * DV;
     const float sl = p.scale_log2;
     bool ok = true;
     int mine = 0;     // S tiles of this query tile before
@@ -467,27 +591,56 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (n == 0) continue;
       const int tok = it.tok0 + x * T + row_tok;
       const int lim = min(tok, it.len - 1);  // last visible key (inclusive)
+      const int warp_lim0 = __shfl_sync(0xffffffffu, lim, 0), warp_lim = __shfl_sync(0xffffffffu, lim, 31);
       float m = -INFINITY;  // running max of score * scale * log2(e)
       float l = 0.f;        // running denominator, relative to 2^m
       for (int j = 0; j < n; ++j) {
+        // Takes the tile's row maximum into the reference m, which moves only when
+        // it has grown by more than 2^8 (exact either way: numerator and
+        // denominator share it); O and the denominator are then rescaled.  O is
+        // idle here: PV(x, j-1) completed before S(x, j) was committed, and
+        // PV(x, j) waits for this group's P.  True if a row of the warp moved.
+        auto raise = [&](float mx) {
+          const float m_new = fmaxf(m, mx * sl);
+          const bool need = m_new > m + kRescaleThreshold || (m == -INFINITY && m_new > -INFINITY);
+          if (!__any_sync(0xffffffffu, need)) return false;
+          const float f = need ? ex2_approx(m - m_new) : 1.f;
+          if (need) {
+            l *= f;
+            m = m_new;
+          }
+          if (j == 0) return true;
+#pragma unroll 1
+          for (int q = 0; q < DV / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * q, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(tO + 32 * q, o);
+          }
+          return true;
+        };
         if (!(ok = warp_wait(bar(S::B_S + x), (mine + j) & 1, p.status, abort_flag))) break;
         tc_fence_after();
-        uint32_t u[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, u[q]);
-        tmem_ld_wait();
-        float sv[128];
-#pragma unroll
-        for (int c = 0; c < 128; ++c) sv[c] = __uint_as_float(u[c >> 5][c & 31]);
         const int key0 = j * kTileN;
-        if (key0 + kTileN - 1 > lim) {
+        if (PAIR && j > 0 && key0 + kTileN - 1 <= warp_lim0) {
+          // A tile that every row sees whole, in the middle of a sequence: the
+          // row stays in registers and the first part's exponentials use the running
+          // maximum while the tile's own is computed (see the chunk kernel).
+          uint32_t u[4][32];
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (key0 + c > lim) sv[c] = -INFINITY;
-        }
-        // Row max: eight independent chains of 3-input max, then a tree (the
-        // last step takes four pairs twice, which leaves the maximum unchanged).
-        auto row_max = [&]() {
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, u[q]);
+          tmem_ld_wait();
+          float sv[128];
+#pragma unroll
+          for (int c = 0; c < 128; ++c) sv[c] = __uint_as_float(u[c >> 5][c & 31]);
+          const float2 sl2 = make_float2(sl, sl);
+          float2 rs4[4];
+          float mb = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) rs4[k] = make_float2(0.f, 0.f);
+          exps_to_tmem<0, S::KP0, false>(sv, sl2, make_float2(-mb, -mb), rs4, tS);
           float mx8[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx8[k] = sv[k];
@@ -495,67 +648,85 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int c = 8; c + 16 <= 128; c += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], sv[c + 2 * k], sv[c + 2 * k + 1]);
+          // (the last step takes four pairs twice, which leaves the maximum unchanged)
 #pragma unroll
           for (int k = 0; k < 8; ++k) mx8[k] = fmax3(mx8[k], sv[120 + 2 * (k & 3)], sv[121 + 2 * (k & 3)]);
-          return fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
-        };
-        const float2 sl2 = make_float2(sl, sl);
-        float2 rs4[4];
-        auto part = [&](auto k0, auto k1, float mref) {
-          const float mb = (mref == -INFINITY) ? 0.f : mref;
-          const float2 nmb2 = make_float2(-mb, -mb);
-          exps_to_tmem<decltype(k0)::value, decltype(k1)::value, false>(sv, sl2, nmb2, rs4, tS);
-        };
-        using K_0 = std::integral_constant<int, 0>;
-        using K_P0 = std::integral_constant<int, S::KP0>;
-        using K_N = std::integral_constant<int, kTileN>;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) rs4[k] = make_float2(0.f, 0.f);
-        if (j == 0) {
-          m = row_max() * sl;
-          part(K_0{}, K_P0{}, m);
-        } else {
-          // The first part's exponentials use the running max right away; only
-          // when the tile's own max has grown by more than 2^8 are O, the
-          // denominator and that part redone (exact either way: numerator and
-          // denominator share the reference m).
-          part(K_0{}, K_P0{}, m);
-          const float m_new = fmaxf(m, row_max() * sl);
-          const bool need = m_new > m + kRescaleThreshold;
-          if (__any_sync(0xffffffffu, need)) {
-            // O is idle here: PV(x, j-1) completed before S(x, j) was
-            // committed, and PV(x, j) waits for this group's P.
-            const float f = need ? ex2_approx(m - m_new) : 1.f;
-            if (need) {
-              l *= f;
-              m = m_new;
-            }
-            tmem_st_wait();
-#pragma unroll
-            for (int q = 0; q < DV / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(tO + 32 * q, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st32(tO + 32 * q, o);
-            }
+          const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7]));
+          if (raise(mx)) {
+            mb = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int k = 0; k < 4; ++k) rs4[k] = make_float2(0.f, 0.f);
-            part(K_0{}, K_P0{}, m);  // rows whose m did not move recompute the same values
+            tmem_st_wait();
+            // rows whose reference did not move recompute the same values
+            exps_to_tmem<0, S::KP0, false>(sv, sl2, make_float2(-mb, -mb), rs4, tS);
           }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(S::B_P + x));
-        if (S::SPLIT_P) {
-          part(K_P0{}, K_N{}, m);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(bar(S::B_P1 + x));
+          mbar_arrive(bar(S::B_P + x));
+          if (S::SPLIT_P) {
+            exps_to_tmem<S::KP0, kTileN, false>(sv, sl2, make_float2(-mb, -mb), rs4, tS);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar(S::B_P1 + x));
+          }
+          const float2 rs2 = fadd2(fadd2(rs4[0], rs4[1]), fadd2(rs4[2], rs4[3]));
+          l += rs2.x + rs2.y;
+          continue;
         }
-        const float2 rs2 = fadd2(fadd2(rs4[0], rs4[1]), fadd2(rs4[2], rs4[3]));
-        l += rs2.x + rs2.y;
+        // The first tile and those on the diagonal, in a loop over chunks of 32
+        // keys that leaves out the chunks that no row of the warp sees (from
+        // `hidden` on; lim rises with the row).  A loop, because this path and the
+        // one above, both unrolled, outgrow the instruction cache when every item is
+        // a few tiles: 64 prompts of 512 tokens took 303 us, this way 199 us.
+        const int hidden = min(4, (warp_lim - key0) / 32 + 1);
+        // ---- row maximum
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < hidden; ++c) {
+          float s[32];
+          load_scores(tS + 32 * c, key0 + 32 * c, lim, s);
+          float m4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmax3(s[k], s[4 + k], s[8 + k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], s[12 + k], s[16 + k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmax3(m4[k], s[20 + k], s[24 + k]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(m4[k], s[28 + k]);
+          mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        }
+        raise(mx);
+        // ---- P, over the S columns already read: chunk c's 16 columns of bf16
+        // pairs lie at or before its 32 columns of scores
+        const float mb = m == -INFINITY ? 0.f : m;
+        const float2 sl2 = make_float2(sl, sl), nmb2 = make_float2(-mb, -mb);
+        float2 rs[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+          if (c < hidden) {
+            float s[32];
+            load_scores(tS + 32 * c, key0 + 32 * c, lim, s);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 e = ffma2(make_float2(s[2 * k], s[2 * k + 1]), sl2, nmb2);
+              const float2 pv = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+              rs[k & 1] = fadd2(rs[k & 1], pv);
+              pk[k] = pack_bf16x2(pv.x, pv.y);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) pk[k] = 0u;
+          }
+          tmem_st16(tS + 16 * c, pk);
+          if (c == 3 || (S::SPLIT_P && c == S::KP0 / 32 - 1)) {
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar((S::SPLIT_P && c == 3 ? S::B_P1 : S::B_P) + x));
+          }
+        }
+        l += (rs[0].x + rs[0].y) + (rs[1].x + rs[1].y);
       }
       if (!ok) break;
       mine += n;
@@ -567,22 +738,33 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const bool valid = tok < it.len && row < G * T;
       const int hq = it.g * G + row_head;
       const float inv = 1.f / l;
-      uint16_t* orow = p.out + (static_cast<int64_t>(it.start + tok) * p.heads + hq) * DV;
+      // A thread holds a row, whose direct 16-byte stores would touch 32 lines
+      // an instruction (3 us an item).  Each 32 dims are transposed within groups of four lanes
+      // first: lane a of a group gets dims 8a .. 8a + 7 of the group's four
+      // rows, and four lanes store 64 consecutive bytes of one row.
+      const int a = lane & 3;
+      uint16_t* dst[4];  // this lane's piece of the group's row k, null for rows that are not stored
 #pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = wq * 32 + (lane & ~3) + k;
+        const int t = it.tok0 + x * T + r / G;
+        dst[k] = t < it.len && r < G * T
+                     ? p.out + (static_cast<int64_t>(it.start + t) * p.heads + it.g * G + r % G) * DV + 8 * a
+                     : nullptr;
+      }
+#pragma unroll 1
       for (int q = 0; q < DV / 32; ++q) {
         uint32_t o[32];
         tmem_ld32(tO + 32 * q, o);
         tmem_ld_wait();
-        uint32_t pk[16];
+        uint32_t w[4][4];  // [piece of 8 dims][word]
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          pk[k] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
-        if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + 32 * q);
+          w[k >> 2][k & 3] = pack_bf16x2(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+        transpose4(w, a);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pk[4 * k], pk[4 * k + 1], pk[4 * k + 2], pk[4 * k + 3]);
-        }
+        for (int k = 0; k < 4; ++k)
+          if (dst[k]) *reinterpret_cast<uint4*>(dst[k] + 32 * q) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
       }
       if (valid && p.lse) p.lse[static_cast<int64_t>(hq) * p.total + it.start + tok] = m * kLn2 + logf(l);
       tc_fence_before();
@@ -596,7 +778,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
     tc_fence_before();
     if (lane == 0) mbar_arrive(bar(S::B_END));
-  } else if ((warp == 1 || warp == 3) && lane == 0) {
+  } else if ((warp == 1 || (PAIR && warp == 3)) && lane == 0) {
     tc_fence_before();
     mbar_arrive(bar(S::B_END));
   }
@@ -607,39 +789,60 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tbase, 512);
+    tmem_dealloc(tbase, S::TMEM_COLS);
   }
 }
 
-template <int DQ, int DV>
+template <int DQ, int DV, bool PAIR>
 cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                            const PromptParams& p, int grid, cudaStream_t stream) {
-  constexpr int smem = PShape<DQ, DV>::SMEM;
+                            const PromptParams& p, cudaStream_t stream) {
+  using S = PShape<DQ, DV, PAIR>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static bool configured[64] = {};
   if (dev < 64 && !configured[dev]) {
-    e = cudaFuncSetAttribute(prompt_attn_kernel<DQ, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(prompt_attn_kernel<DQ, DV, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  prompt_attn_kernel<DQ, DV><<<grid, kAttnThreads, smem, stream>>>(tm_q, tm_k, tm_v, p);
+  // Items: at most one for each whole tile (pair) of the rows and one partial
+  // one for each sequence.
+  const int64_t tokens = S::TILES * (kTileM / (p.heads / p.kv_heads));
+  const int64_t items = (p.total / tokens + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
+  if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
+  prompt_attn_kernel<DQ, DV, PAIR><<<static_cast<int>(items), S::THREADS, S::SMEM, stream>>>(tm_q, tm_k, tm_v, p);
   return cudaGetLastError();
+}
+
+// One query tile a CTA, two CTAs per SM, where the second tile of a pair would
+// mostly be absent (sequences of up to T tokens on average: 1024 prompts of 32
+// tokens, 32/8 heads, take 136 us, in pairs 210), and where every tile can have an
+// SM of its own (one prompt of 77 tokens 7.9 us, in pairs 8.8; of 500 tokens 13.8
+// and 15.2).  Otherwise pairs, which read each key tile half as often (32 prompts of
+// 1024 tokens: 302 us against 329; one of 16384: 1437 us against 1994).
+template <int DQ, int DV>
+cudaError_t launch_prompt_d(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                            const PromptParams& p, int num_sms, cudaStream_t stream) {
+  if constexpr (DQ <= 128) {  // (three stages of 192 dims do not fit half an SM)
+    const int64_t T = kTileM / (p.heads / p.kv_heads);
+    const int64_t tiles = (p.total / T + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
+    if (p.total <= T * p.batch || tiles <= num_sms)
+      return launch_prompt_t<DQ, DV, false>(tm_q, tm_k, tm_v, p, stream);
+  }
+  return launch_prompt_t<DQ, DV, true>(tm_q, tm_k, tm_v, p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_prompt_attn(int dq, int dv, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                               const CUtensorMap& tm_v, const PromptParams& p, int64_t items, int num_sms,
-                               cudaStream_t stream) {
-  const int grid = static_cast<int>(std::min<int64_t>(items * p.kv_heads, num_sms));
-  if (dq == 64 && dv == 64) return launch_prompt_t<64, 64>(tm_q, tm_k, tm_v, p, grid, stream);
-  if (dq == 64 && dv == 128) return launch_prompt_t<64, 128>(tm_q, tm_k, tm_v, p, grid, stream);
-  if (dq == 128 && dv == 64) return launch_prompt_t<128, 64>(tm_q, tm_k, tm_v, p, grid, stream);
-  if (dq == 128 && dv == 128) return launch_prompt_t<128, 128>(tm_q, tm_k, tm_v, p, grid, stream);
-  if (dq == 192 && dv == 64) return launch_prompt_t<192, 64>(tm_q, tm_k, tm_v, p, grid, stream);
-  if (dq == 192 && dv == 128) return launch_prompt_t<192, 128>(tm_q, tm_k, tm_v, p, grid, stream);
+                               const CUtensorMap& tm_v, const PromptParams& p, int num_sms, cudaStream_t stream) {
+  if (dq == 64 && dv == 64) return launch_prompt_d<64, 64>(tm_q, tm_k, tm_v, p, num_sms, stream);
+  if (dq == 64 && dv == 128) return launch_prompt_d<64, 128>(tm_q, tm_k, tm_v, p, num_sms, stream);
+  if (dq == 128 && dv == 64) return launch_prompt_d<128, 64>(tm_q, tm_k, tm_v, p, num_sms, stream);
+  if (dq == 128 && dv == 128) return launch_prompt_d<128, 128>(tm_q, tm_k, tm_v, p, num_sms, stream);
+  if (dq == 192 && dv == 64) return launch_prompt_d<192, 64>(tm_q, tm_k, tm_v, p, num_sms, stream);
+  if (dq == 192 && dv == 128) return launch_prompt_d<192, 128>(tm_q, tm_k, tm_v, p, num_sms, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -23,9 +23,7 @@ struct PromptParams {
 };
 
 // Query rows of a tile: kTileM / G tokens of the G heads of a kv head.
-// items: an upper bound of the (sequence, tile pair) count.
 cudaError_t launch_prompt_attn(int dq, int dv, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                               const CUtensorMap& tm_v, const PromptParams& p, int64_t items, int num_sms,
-                               cudaStream_t stream);
+                               const CUtensorMap& tm_v, const PromptParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace vpp
