@@ -28,12 +28,14 @@
 //               last page of a sequence in boxes of 16 tokens, so that a short
 //               sequence does not read 64 rows for a few.  It looks up the
 //               block table 32 pages at a time.
-//   warps 0-3   tokens 16 w .. 16 w + 15 of the page: S = Q K^T and O += P V on
-//               the warp-level tensor cores (mma.sync m16n8k16, float32
-//               accumulation).  The 16 rows are the group's query heads (zeros past
-//               G), K and V come by ldmatrix from the swizzled stage, and P
-//               goes from the accumulators of S to the operand of P V in
-//               registers.  The decode products need a few per cent of even this
+//   warps 0-3   tokens 16 w .. 16 w + 15 of the page: S^T = K Q^T and O^T += V^T P^T
+//               on the warp-level tensor cores (mma.sync m16n8k16, float32
+//               accumulation).  The 16 rows are tokens, then dims, the 8 columns query
+//               heads (a group of 9 to 16 takes two products).  K and V come by
+//               ldmatrix from the swizzled stage, and P^T goes from the
+//               accumulators of S^T to the operand in registers.  (With the heads
+//               as the rows, half of them empty for 8 heads, an E4M3 cache read
+//               15% slower.)  The decode products need a few per cent of even this
 //               tensor path; tcgen05's 128-row tiles would be 1/8 to 1/128 full.
 // The four warps' running results are joined through shared memory at the end
 // of each sequence.
@@ -42,6 +44,7 @@
 // is an f16 value) after ldmatrix; q is scaled per head by a power of two into f16's
 // range; k_scale joins the score scale and v_scale the result.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -57,7 +60,8 @@ constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kCtasPerSm = 2;
 constexpr int kRingBytes = 96 * 1024;
 
-template <int DQ, int DV, bool F8>
+// NG: query heads in groups of 8 (a kv head's G heads fill one or two).
+template <int DQ, int DV, bool F8, int NG>
 struct Cfg {
   static constexpr int ESZ = F8 ? 1 : 2;
   // Bytes of a slab row: 64 bf16 values, 128 codes (or 64 where the head dim
@@ -69,9 +73,9 @@ struct Cfg {
   static constexpr int KBYTES = DQ * ESZ * kBlockTokens;
   static constexpr int STAGE = KBYTES + DV * ESZ * kBlockTokens;
   static constexpr int NST = kRingBytes / STAGE > 8 ? 8 : kRingBytes / STAGE;
-  static constexpr int KS = DQ / 16;  // k-steps of S
-  static constexpr int NT = DV / 8;   // 8-dim tiles of O
-  static constexpr int CSTRIDE = DV + 4;  // row stride of the join buffer: at most 2 lanes on a bank
+  static constexpr int KS = DQ / 16;  // 16-dim steps of S^T
+  static constexpr int NT = DV / 16;  // 16-dim tiles of O^T
+  static constexpr int CSTRIDE = DV + 4;  // row stride of the join buffer: no two lanes of a store on a bank
   static constexpr int COMB = kConsumers * 8 * CSTRIDE * 4;
   static constexpr int SMEM = NST * STAGE + COMB + kConsumers * 8 * 8 + 2 * NST * 8 + 48;
   static_assert(NST >= 2, "two stages at least");
@@ -114,6 +118,14 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 template <int ROW>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
   return ROW == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// Transposes an 8x8 matrix of 16-bit values held one row pair per lane
+// (lane 4 r + c: row r, columns 2c and 2c + 1).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // One thing the join kernel adds up: the parts of sequence b in columns
@@ -173,12 +185,12 @@ struct SeqWalk {
   }
 };
 
-template <int DQ, int DV, bool F8>
+template <int DQ, int DV, bool F8, int NG>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                         const __grid_constant__ PagedDecodeParams p, const Workspace ws, const int cols) {
-  using C = Cfg<DQ, DV, F8>;
+  using C = Cfg<DQ, DV, F8, NG>;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* comb = reinterpret_cast<float*>(smem + C::NST * C::STAGE);                  // [4][8][CSTRIDE]
   float2* ml = reinterpret_cast<float2*>(smem + C::NST * C::STAGE + C::COMB);        // [4][8]
@@ -362,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const float sl = F8 ? p.scale_log2 * __ldg(p.k_scale + h) : p.scale_log2;
   const float vsc = F8 ? __ldg(p.v_scale + h) : 1.f;
   const uint32_t ring = smem_u32(smem);
-  // rows of this lane's ldmatrix addresses: K pairs (token half, chunk), V
-  // pairs (chunk, token half); codes pair (chunk, token half) in both
-  const int krow = warp * 16 + (F8 ? (mi & 1) : (mi >> 1)) * 8 + r8;
-  const int vrow = warp * 16 + (mi & 1) * 8 + r8;
+  // Rows and chunks of this lane's ldmatrix addresses.  K (and V's codes): token halves,
+  // then chunks; V: chunks, then token halves.
+  const int krow = warp * 16 + (mi & 1) * 8 + r8, kchunk = mi >> 1;
+  const int vrow = F8 ? krow : warp * 16 + (mi >> 1) * 8 + r8, vchunk = F8 ? kchunk : mi & 1;
 
   SeqWalk sw;
   sw.start(p, start_b);
@@ -376,26 +388,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   while (left > 0) {
     const int seq_pages = pages_of(sw.ctx);
     const int np = min(seq_pages - page, left);
-    // ---- q of the sequence as the A operand: rows g and g + 8
-    uint32_t qa[C::KS][4];
-    float rs[2] = {sl, sl};  // score scale of the two rows
+    // ---- q of the sequence as the B operand: column g is head g of the group
+    uint32_t qb[NG][C::KS][2];
+    float rs[NG][2];  // score scale of this thread's columns, heads 2u and 2u + 1
     {
       const uint16_t* qrow = p.q + sw.b * p.q_stride + static_cast<int64_t>(h) * G * DQ;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const bool live = g + 8 * r < G;
-        const uint16_t* src = qrow + (live ? g + 8 * r : 0) * DQ;
+      for (int n = 0; n < NG; ++n) {
+        const bool live = 8 * n + g < G;
+        const uint16_t* src = qrow + (live ? 8 * n + g : 0) * DQ;
         if (!F8) {
 #pragma unroll
           for (int s = 0; s < C::KS; ++s) {
             const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u));
             const uint32_t hi = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u + 8));
-            qa[s][r] = live ? lo : 0u;
-            qa[s][2 + r] = live ? hi : 0u;
+            qb[n][s][0] = live ? lo : 0u;
+            qb[n][s][1] = live ? hi : 0u;
           }
+          rs[n][0] = rs[n][1] = sl;
         } else {
-          // codes 4u .. 4u + 3 of a 16-dim step are a lane's (see the K
-          // operand), and the row is scaled by 2^e so that its largest |q| is in
+          // dims 4u .. 4u + 3 of a 16-dim step are a lane's (see the K operand),
+          // and the head is scaled by 2^e so that its largest |q| is in
           // [2^14, 2^15): below f16's largest value, and every bf16 value that is
           // not negligible beside it keeps its 8 significant bits
           const uint2* src4 = reinterpret_cast<const uint2*>(src + 4 * u);
@@ -403,147 +416,178 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
           for (int s = 0; s < C::KS; ++s) {
             const uint2 w = __ldg(src4 + 4 * s);
-            qa[s][r] = live ? w.x : 0u;
-            qa[s][2 + r] = live ? w.y : 0u;
+            qb[n][s][0] = live ? w.x : 0u;
+            qb[n][s][1] = live ? w.y : 0u;
             amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))),
                                      fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y)))));
           }
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
           const int e = (amax > 0.f && amax < INFINITY) ? max(-60, min(60, 14 - ilogbf(amax))) : 0;
-          const float up = ldexpf(1.f, e);
-          rs[r] = sl * ldexpf(1.f, -e);
+          const float up = ldexpf(1.f, e), down = sl * ldexpf(1.f, -e);
+          rs[n][0] = __shfl_sync(0xffffffffu, down, 8 * u);  // lane 4 (2u) holds head 2u
+          rs[n][1] = __shfl_sync(0xffffffffu, down, 8 * u + 4);
 #pragma unroll
           for (int s = 0; s < C::KS; ++s) {
-            qa[s][r] = pack_half2(bf16_lo(qa[s][r]) * up, bf16_hi(qa[s][r]) * up);
-            qa[s][2 + r] = pack_half2(bf16_lo(qa[s][2 + r]) * up, bf16_hi(qa[s][2 + r]) * up);
+            qb[n][s][0] = pack_half2(bf16_lo(qb[n][s][0]) * up, bf16_hi(qb[n][s][0]) * up);
+            qb[n][s][1] = pack_half2(bf16_lo(qb[n][s][1]) * up, bf16_hi(qb[n][s][1]) * up);
           }
         }
       }
     }
-    float m[2] = {-INFINITY, -INFINITY};
-    float l[2] = {0.f, 0.f};  // this lane's part of the denominators
-    float o[C::NT][4];
+    float m[NG][2], l[NG][2];  // running maxima, and this lane's part of the denominators
+    float o[NG][C::NT][4];
 #pragma unroll
-    for (int n = 0; n < C::NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    for (int n = 0; n < NG; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int t = 0; t < C::NT; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
+    }
+
+    // 16 tokens of a stage, `live` of them keys of the sequence (all, unless TAIL).
+    auto step = [&](auto tail, uint32_t kb, int live) {
+      constexpr bool TAIL = decltype(tail)::value;
+      const uint32_t vb = kb + C::KBYTES;
+      // ---- S^T = K Q^T, 16 tokens x 8 heads; two accumulator chains
+      float s[NG][2][4];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) s[n][c][0] = s[n][c][1] = s[n][c][2] = s[n][c][3] = 0.f;
+      if (!F8) {
+#pragma unroll
+        for (int k = 0; k < C::KS; ++k) {
+          uint32_t r[4];
+          ldsm4(kb + (k >> 2) * 128 * kBlockTokens + swz<128>(krow, 2 * (k & 3) + kchunk), r);
+#pragma unroll
+          for (int n = 0; n < NG; ++n) mma<false>(s[n][k & 1], r, qb[n][k][0], qb[n][k][1]);
+        }
+      } else {
+        constexpr int CPS = C::KROW / 16;  // 16-code chunks of a slab row
+#pragma unroll
+        for (int k = 0; k < C::KS; k += 2) {
+          uint32_t r[4];
+          ldsm4(kb + (k / CPS) * C::KROW * kBlockTokens + swz<C::KROW>(krow, k % CPS + kchunk), r);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t a[4];
+            e4m3x4_to_f16x2x2(r[2 * x], a[0], a[2]);
+            e4m3x4_to_f16x2x2(r[2 * x + 1], a[1], a[3]);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) mma<true>(s[n][x], a, qb[n][k + x][0], qb[n][k + x][1]);
+          }
+        }
+      }
+      uint32_t pb[NG][2];  // P^T as the B operand
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        // ---- scores in log2 units: [e >> 1: token g or g + 8][e & 1: head];
+        // keys past the sequence leave the softmax
+        float sc[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[e] = (s[n][0][e] + s[n][1][e]) * rs[n][e & 1];
+          if (TAIL && g + 8 * (e >> 1) >= live) sc[e] = -INFINITY;
+        }
+        // ---- online softmax of the two heads (eight lanes hold a head); the
+        // reference moves only when the maximum has grown by more than 2^8
+        float f[2];
+        bool moved = false;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float mx = fmaxf(sc[c], sc[2 + c]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          f[c] = 1.f;
+          if (mx > m[n][c] + 8.0f || (m[n][c] == -INFINITY && mx > -INFINITY)) {
+            f[c] = ex2_approx(m[n][c] - mx);
+            m[n][c] = mx;
+            moved = true;
+          }
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+          l[n][0] *= f[0];
+          l[n][1] *= f[1];
+#pragma unroll
+          for (int t = 0; t < C::NT; ++t) {
+            o[n][t][0] *= f[0];
+            o[n][t][1] *= f[1];
+            o[n][t][2] *= f[0];
+            o[n][t][3] *= f[1];
+          }
+        }
+        float pv[4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float mr = m[n][c] == -INFINITY ? 0.f : m[n][c];
+          pv[c] = ex2_approx(sc[c] - mr);
+          pv[2 + c] = ex2_approx(sc[2 + c] - mr);
+          l[n][c] += pv[c] + pv[2 + c];
+        }
+        // P is rounded to the operand type of V; the denominator keeps float32.
+        // Its accumulator fragment, transposed, is the operand's.
+        pb[n][0] = transpose8x8(F8 ? pack_half2(pv[0], pv[1]) : pack_bf16x2(pv[0], pv[1]));
+        pb[n][1] = transpose8x8(F8 ? pack_half2(pv[2], pv[3]) : pack_bf16x2(pv[2], pv[3]));
+      }
+      // ---- O^T += V^T P^T.  Rows past the sequence may hold anything, and P = 0
+      // times them must stay 0: their halves of the operand words are cleared.
+      uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+      if (TAIL) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int at = 8 * t + 2 * u;
+          mask[t] = (at < live ? 0x0000FFFFu : 0u) | (at + 1 < live ? 0xFFFF0000u : 0u);
+        }
+      }
+      if (!F8) {
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t) {
+          uint32_t r[4];
+          ldsm4_t(vb + (t >> 2) * 128 * kBlockTokens + swz<128>(vrow, 2 * (t & 3) + vchunk), r);
+          if (TAIL) {
+            r[0] &= mask[0];
+            r[1] &= mask[0];
+            r[2] &= mask[1];
+            r[3] &= mask[1];
+          }
+#pragma unroll
+          for (int n = 0; n < NG; ++n) mma<false>(o[n][t], r, pb[n][0], pb[n][1]);
+        }
+      } else {
+        // A word holds dims 2g, 2g + 1 of tokens 2u, 2u + 1: row g of the tile is
+        // dim 2g of a 16-dim chunk, row g + 8 dim 2g + 1.
+        constexpr int CPS = C::VROW / 16;
+#pragma unroll
+        for (int t = 0; t < C::NT; t += 2) {
+          uint32_t r[4];
+          ldsm4_t(vb + (t / CPS) * C::VROW * kBlockTokens + swz<C::VROW>(vrow, t % CPS + vchunk), r);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t a[4];
+            if (TAIL) {
+              r[2 * x] &= mask[0];
+              r[2 * x + 1] &= mask[1];
+            }
+            e4m3x4_to_f16x2x2(__byte_perm(r[2 * x], 0u, 0x3120u), a[0], a[1]);
+            e4m3x4_to_f16x2x2(__byte_perm(r[2 * x + 1], 0u, 0x3120u), a[2], a[3]);
+#pragma unroll
+            for (int n = 0; n < NG; ++n) mma<true>(o[n][t + x], a, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+    };
 
     for (int i = 0; i < np; ++i) {
       // tokens of this warp's 16 that are keys of the sequence
       const int live = sw.ctx - (page + i) * kBlockTokens - warp * 16;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars[slot]), phase, p.status, abort_flag));
-      if (ok && live > 0) {
-        const uint32_t kb = ring + slot * C::STAGE, vb = kb + C::KBYTES;
-        // ---- S = Q K^T: two 8-token tiles, two accumulator chains each
-        float s[2][2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) s[t][c][0] = s[t][c][1] = s[t][c][2] = s[t][c][3] = 0.f;
-        if (!F8) {
-#pragma unroll
-          for (int k = 0; k < C::KS; ++k) {
-            uint32_t r[4];
-            ldsm4(kb + (k >> 2) * 128 * kBlockTokens + swz<128>(krow, 2 * (k & 3) + (mi & 1)), r);
-            mma<false>(s[0][k & 1], qa[k], r[0], r[1]);
-            mma<false>(s[1][k & 1], qa[k], r[2], r[3]);
-          }
-        } else {
-          constexpr int CPS = C::KROW / 16;  // 16-code chunks of a slab row
-#pragma unroll
-          for (int k = 0; k < C::KS; k += 2) {
-            uint32_t r[4], lo, hi;
-            ldsm4(kb + (k / CPS) * C::KROW * kBlockTokens + swz<C::KROW>(krow, k % CPS + (mi >> 1)), r);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              e4m3x4_to_f16x2x2(r[x], lo, hi);
-              mma<true>(s[x & 1][x >> 1], qa[k + (x >> 1)], lo, hi);
-            }
-          }
-        }
-        // ---- scores in log2 units; keys past the sequence leave the softmax
-        float sc[2][4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v = (s[t][0][e] + s[t][1][e]) * rs[e >> 1];
-            sc[t][e] = 8 * t + 2 * u + (e & 1) < live ? v : -INFINITY;
-          }
-        // ---- online softmax of rows g and g + 8 (four lanes hold a row); the
-        // reference moves only when the maximum has grown by more than 2^8
-        float f[2];
-        bool moved = false;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float mx = fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          f[r] = 1.f;
-          if (mx > m[r] + 8.0f || (m[r] == -INFINITY && mx > -INFINITY)) {
-            f[r] = ex2_approx(m[r] - mx);
-            m[r] = mx;
-            moved = true;
-          }
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-          l[0] *= f[0];
-          l[1] *= f[1];
-#pragma unroll
-          for (int n = 0; n < C::NT; ++n) {
-            o[n][0] *= f[0];
-            o[n][1] *= f[0];
-            o[n][2] *= f[1];
-            o[n][3] *= f[1];
-          }
-        }
-        uint32_t pa[4];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float mr = m[r] == -INFINITY ? 0.f : m[r];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const float a = ex2_approx(sc[t][2 * r] - mr), b = ex2_approx(sc[t][2 * r + 1] - mr);
-            l[r] += a + b;
-            // P is rounded to the operand type of V; the denominator keeps float32
-            pa[2 * t + r] = F8 ? pack_half2(a, b) : pack_bf16x2(a, b);
-          }
-        }
-        // ---- O += P V.  Rows past the sequence may hold anything, and P = 0
-        // times them must stay 0: their halves of the operand words are cleared.
-        uint32_t mask[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (live < 16) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int at = 8 * t + 2 * u;
-            mask[t] = (at < live ? 0x0000FFFFu : 0u) | (at + 1 < live ? 0xFFFF0000u : 0u);
-          }
-        }
-        if (!F8) {
-#pragma unroll
-          for (int n = 0; n < C::NT; n += 2) {
-            uint32_t r[4];
-            ldsm4_t(vb + (n >> 3) * 128 * kBlockTokens + swz<128>(vrow, (n & 7) + (mi >> 1)), r);
-            mma<false>(o[n], pa, r[0] & mask[0], r[1] & mask[1]);
-            mma<false>(o[n + 1], pa, r[2] & mask[0], r[3] & mask[1]);
-          }
-        } else {
-          // A word holds dims 2g, 2g + 1 of tokens 2u, 2u + 1: tile n takes the
-          // even dims of a 16-dim chunk, tile n + 1 the odd ones.
-          constexpr int CPS = C::VROW / 16;
-#pragma unroll
-          for (int c = 0; c < DV / 16; c += 2) {
-            uint32_t r[4];
-            ldsm4_t(vb + (c / CPS) * C::VROW * kBlockTokens + swz<C::VROW>(vrow, c % CPS + (mi >> 1)), r);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t e0, d0, e1, d1;
-              e4m3x4_to_f16x2x2(__byte_perm(r[2 * x] & mask[0], 0u, 0x3120u), e0, d0);
-              e4m3x4_to_f16x2x2(__byte_perm(r[2 * x + 1] & mask[1], 0u, 0x3120u), e1, d1);
-              mma<true>(o[2 * (c + x)], pa, e0, e1);
-              mma<true>(o[2 * (c + x) + 1], pa, d0, d1);
-            }
-          }
-        }
+      if (ok) {
+        if (live >= 16)
+          step(std::false_type{}, ring + slot * C::STAGE, 16);
+        else if (live > 0)
+          step(std::true_type{}, ring + slot * C::STAGE, live);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars[C::NST + slot]));
@@ -557,23 +601,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // every sequence, also after a failed wait, so the barriers match.
     const bool whole = np == seq_pages;
     const int part = (col * 2 + (page == start_page && left == n_pages ? 0 : 1));
-    for (int half = 0; half < (G > 8 ? 2 : 1); ++half) {
-      float lr = l[half];
-      lr += __shfl_xor_sync(0xffffffffu, lr, 1);
-      lr += __shfl_xor_sync(0xffffffffu, lr, 2);
-      if (u == 0) ml[warp * 8 + g] = make_float2(m[half], lr);
-      float* dst = comb + (warp * 8 + g) * C::CSTRIDE;
-      if (!F8) {
 #pragma unroll
-        for (int n = 0; n < C::NT; ++n)
-          *reinterpret_cast<float2*>(dst + 8 * n + 2 * u) =
-              half ? make_float2(o[n][2], o[n][3]) : make_float2(o[n][0], o[n][1]);
-      } else {
+    for (int half = 0; half < NG; ++half) {
 #pragma unroll
-        for (int n = 0; n < C::NT; n += 2)
-          *reinterpret_cast<float4*>(dst + 8 * n + 4 * u) =
-              half ? make_float4(o[n][2], o[n + 1][2], o[n][3], o[n + 1][3])
-                   : make_float4(o[n][0], o[n + 1][0], o[n][1], o[n + 1][1]);
+      for (int c = 0; c < 2; ++c) {
+        float lr = l[half][c];
+        lr += __shfl_xor_sync(0xffffffffu, lr, 4);
+        lr += __shfl_xor_sync(0xffffffffu, lr, 8);
+        lr += __shfl_xor_sync(0xffffffffu, lr, 16);
+        if (g == 0) ml[warp * 8 + 2 * u + c] = make_float2(m[half][c], lr);
+        float* dst = comb + (warp * 8 + 2 * u + c) * C::CSTRIDE;
+#pragma unroll
+        for (int t = 0; t < C::NT; ++t) {
+          if (!F8) {
+            dst[16 * t + g] = o[half][t][c];
+            dst[16 * t + 8 + g] = o[half][t][2 + c];
+          } else {
+            *reinterpret_cast<float2*>(dst + 16 * t + 2 * g) = make_float2(o[half][t][c], o[half][t][2 + c]);
+          }
+        }
       }
       asm volatile("bar.sync 1, 128;" ::: "memory");
       constexpr int PER = DV / 16;  // dims of a thread: 16 threads a row
@@ -707,20 +753,20 @@ int decode_cols(int kv_heads, int num_sms) {
   return best;
 }
 
-template <int DQ, int DV, bool F8>
+template <int DQ, int DV, bool F8, int NG>
 cudaError_t launch_t(const PagedDecodeParams& p, const CUtensorMap* maps, const Workspace& ws, int cols,
                      cudaStream_t stream) {
-  using C = Cfg<DQ, DV, F8>;
+  using C = Cfg<DQ, DV, F8, NG>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   static bool configured[64] = {};
   if (dev < 64 && !configured[dev]) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<DQ, DV, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    e = cudaFuncSetAttribute(paged_decode_kernel<DQ, DV, F8, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  paged_decode_kernel<DQ, DV, F8><<<cols * p.kv_heads, kThreads, C::SMEM, stream>>>(maps[0], maps[1], maps[2], maps[3],
+  paged_decode_kernel<DQ, DV, F8, NG><<<cols * p.kv_heads, kThreads, C::SMEM, stream>>>(maps[0], maps[1], maps[2], maps[3],
                                                                                   p, ws, cols);
   e = cudaGetLastError();
   if (e != cudaSuccess || cols == 1) return e;
@@ -760,8 +806,11 @@ cudaError_t launch_paged_decode(const PagedDecodeParams& p, bool fp8, const CUte
   }
 #define VPP_CASE(DQ, DV)                                                             \
   if (p.dq == DQ && p.dv == DV)                                                      \
-    return fp8 ? launch_t<DQ, DV, true>(p, maps, ws, cols, stream)                   \
-               : launch_t<DQ, DV, false>(p, maps, ws, cols, stream);
+    return p.heads / p.kv_heads > 8                                                  \
+               ? (fp8 ? launch_t<DQ, DV, true, 2>(p, maps, ws, cols, stream)         \
+                      : launch_t<DQ, DV, false, 2>(p, maps, ws, cols, stream))       \
+               : (fp8 ? launch_t<DQ, DV, true, 1>(p, maps, ws, cols, stream)         \
+                      : launch_t<DQ, DV, false, 1>(p, maps, ws, cols, stream));
   VPP_CASE(64, 64)
   VPP_CASE(64, 128)
   VPP_CASE(128, 64)
