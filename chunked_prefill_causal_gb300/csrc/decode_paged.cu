@@ -57,8 +57,12 @@ namespace {
 constexpr float kLn2p = 0.69314718055994530942f;
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kCtasPerSm = 2;
-constexpr int kRingBytes = 96 * 1024;
+
+// CTAs per SM: three where a stage is small and one group of 8 heads fits 128
+// registers, else two.
+constexpr int ctas_per_sm(int dq, int dv, bool f8, int ng) {
+  return ng == 1 && (dq + dv) * (f8 ? 1 : 2) <= 256 ? 3 : 2;
+}
 
 // NG: query heads in groups of 8 (a kv head's G heads fill one or two).
 template <int DQ, int DV, bool F8, int NG>
@@ -72,14 +76,16 @@ struct Cfg {
   static constexpr int VSLABS = DV * ESZ / VROW;
   static constexpr int KBYTES = DQ * ESZ * kBlockTokens;
   static constexpr int STAGE = KBYTES + DV * ESZ * kBlockTokens;
-  static constexpr int NST = kRingBytes / STAGE > 8 ? 8 : kRingBytes / STAGE;
+  static constexpr int CTAS = ctas_per_sm(DQ, DV, F8, NG);
+  static constexpr int FIT = ((CTAS == 3 ? 56 : 96) * 1024) / STAGE;
+  static constexpr int NST = FIT > 8 ? 8 : FIT;
   static constexpr int KS = DQ / 16;  // 16-dim steps of S^T
   static constexpr int NT = DV / 16;  // 16-dim tiles of O^T
   static constexpr int CSTRIDE = DV + 4;  // row stride of the join buffer: no two lanes of a store on a bank
   static constexpr int COMB = kConsumers * 8 * CSTRIDE * 4;
   static constexpr int SMEM = NST * STAGE + COMB + kConsumers * 8 * 8 + 2 * NST * 8 + 48;
   static_assert(NST >= 2, "two stages at least");
-  static_assert(SMEM + 1024 <= 228 * 1024 / kCtasPerSm, "two CTAs per SM");
+  static_assert(SMEM + 1024 <= 228 * 1024 / CTAS, "CTAs per SM");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -186,7 +192,7 @@ struct SeqWalk {
 };
 
 template <int DQ, int DV, bool F8, int NG>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ CUtensorMap tm_k16, const __grid_constant__ CUtensorMap tm_v16,
                         const __grid_constant__ PagedDecodeParams p, const Workspace ws, const int cols) {
@@ -385,56 +391,62 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   int slot = 0;
   uint32_t phase = 0u;
   bool ok = true;
+  // q of a sequence as the B operand: column g is head g of the group (zeros
+  // past G).  E4M3 cache: dims 4u .. 4u + 3 of a 16-dim step are a lane's (see
+  // the K operand).
+  uint32_t qb[NG][C::KS][2];
+  float rs[NG][2];  // score scale of this thread's columns, heads 2u and 2u + 1
+  auto load_q = [&](int b) {
+    const uint16_t* qrow = p.q + b * p.q_stride + static_cast<int64_t>(h) * G * DQ;
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const bool live = 8 * n + g < G;
+      const uint16_t* src = qrow + (live ? 8 * n + g : 0) * DQ;
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s) {
+        uint2 w;
+        if (F8) {
+          w = __ldg(reinterpret_cast<const uint2*>(src + 16 * s + 4 * u));
+        } else {
+          w.x = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u));
+          w.y = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u + 8));
+        }
+        qb[n][s][0] = live ? w.x : 0u;
+        qb[n][s][1] = live ? w.y : 0u;
+      }
+      rs[n][0] = rs[n][1] = sl;
+    }
+  };
+  // E4M3 cache: bf16 -> f16 in place, a head scaled by 2^e so that its largest
+  // |q| is in [2^14, 2^15): below f16's largest value, and every bf16 value that
+  // is not negligible beside it keeps its 8 significant bits.
+  auto scale_q = [&]() {
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      float amax = 0.f;
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(qb[n][s][i])), fabsf(bf16_hi(qb[n][s][i]))));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = (amax > 0.f && amax < INFINITY) ? max(-60, min(60, 14 - ilogbf(amax))) : 0;
+      const float up = ldexpf(1.f, e), down = sl * ldexpf(1.f, -e);
+      rs[n][0] = __shfl_sync(0xffffffffu, down, 8 * u);  // lane 4 (2u) holds head 2u
+      rs[n][1] = __shfl_sync(0xffffffffu, down, 8 * u + 4);
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          qb[n][s][i] = pack_half2(bf16_lo(qb[n][s][i]) * up, bf16_hi(qb[n][s][i]) * up);
+    }
+  };
+  load_q(start_b);
   while (left > 0) {
     const int seq_pages = pages_of(sw.ctx);
     const int np = min(seq_pages - page, left);
-    // ---- q of the sequence as the B operand: column g is head g of the group
-    uint32_t qb[NG][C::KS][2];
-    float rs[NG][2];  // score scale of this thread's columns, heads 2u and 2u + 1
-    {
-      const uint16_t* qrow = p.q + sw.b * p.q_stride + static_cast<int64_t>(h) * G * DQ;
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const bool live = 8 * n + g < G;
-        const uint16_t* src = qrow + (live ? 8 * n + g : 0) * DQ;
-        if (!F8) {
-#pragma unroll
-          for (int s = 0; s < C::KS; ++s) {
-            const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u));
-            const uint32_t hi = __ldg(reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * u + 8));
-            qb[n][s][0] = live ? lo : 0u;
-            qb[n][s][1] = live ? hi : 0u;
-          }
-          rs[n][0] = rs[n][1] = sl;
-        } else {
-          // dims 4u .. 4u + 3 of a 16-dim step are a lane's (see the K operand),
-          // and the head is scaled by 2^e so that its largest |q| is in
-          // [2^14, 2^15): below f16's largest value, and every bf16 value that is
-          // not negligible beside it keeps its 8 significant bits
-          const uint2* src4 = reinterpret_cast<const uint2*>(src + 4 * u);
-          float amax = 0.f;
-#pragma unroll
-          for (int s = 0; s < C::KS; ++s) {
-            const uint2 w = __ldg(src4 + 4 * s);
-            qb[n][s][0] = live ? w.x : 0u;
-            qb[n][s][1] = live ? w.y : 0u;
-            amax = fmaxf(amax, fmaxf(fmaxf(fabsf(bf16_lo(w.x)), fabsf(bf16_hi(w.x))),
-                                     fmaxf(fabsf(bf16_lo(w.y)), fabsf(bf16_hi(w.y)))));
-          }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          const int e = (amax > 0.f && amax < INFINITY) ? max(-60, min(60, 14 - ilogbf(amax))) : 0;
-          const float up = ldexpf(1.f, e), down = sl * ldexpf(1.f, -e);
-          rs[n][0] = __shfl_sync(0xffffffffu, down, 8 * u);  // lane 4 (2u) holds head 2u
-          rs[n][1] = __shfl_sync(0xffffffffu, down, 8 * u + 4);
-#pragma unroll
-          for (int s = 0; s < C::KS; ++s) {
-            qb[n][s][0] = pack_half2(bf16_lo(qb[n][s][0]) * up, bf16_hi(qb[n][s][0]) * up);
-            qb[n][s][1] = pack_half2(bf16_lo(qb[n][s][1]) * up, bf16_hi(qb[n][s][1]) * up);
-          }
-        }
-      }
-    }
+    if (F8) scale_q();
     float m[NG][2], l[NG][2];  // running maxima, and this lane's part of the denominators
     float o[NG][C::NT][4];
 #pragma unroll
@@ -597,6 +609,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
     }
 
+    // The next sequence's q loads while this one's warps are joined.
+    SeqWalk nx = sw;
+    if (left > np) {
+      nx.next(p);
+      load_q(nx.b);
+    }
     // ---- join the four warps, 8 rows at a time.  Every warp comes here for
     // every sequence, also after a failed wait, so the barriers match.
     const bool whole = np == seq_pages;
@@ -675,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     left -= np;
     page = 0;
-    if (left > 0) sw.next(p);
+    sw = nx;
   }
 }
 
@@ -736,8 +754,7 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
 // that are resident at once.  The smallest number of waves that leaves at most 4%
 // of the places empty (8 kv heads: one wave of 38 columns; 128: three
 // waves of 7), or the fullest of up to four.
-int decode_cols(int kv_heads, int num_sms) {
-  const int places = kCtasPerSm * num_sms;
+int decode_cols(int kv_heads, int places) {
   int best = 1;
   double best_fill = 0.0;
   for (int w = 1; w <= 4; ++w) {
@@ -786,15 +803,18 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
-size_t paged_decode_ws_bytes(int32_t, int heads, int kv_heads, int, int dv, int num_sms) {
-  const size_t cols = decode_cols(kv_heads, num_sms);
+size_t paged_decode_ws_bytes(int32_t, int heads, int kv_heads, int dq, int dv, int num_sms) {
+  const int ng = heads / kv_heads > 8 ? 2 : 1;  // the larger of the two cache types' needs
+  const size_t cols = std::max(decode_cols(kv_heads, num_sms * ctas_per_sm(dq, dv, false, ng)),
+                               decode_cols(kv_heads, num_sms * ctas_per_sm(dq, dv, true, ng)));
   if (cols == 1) return 0;
   return align256(cols * 2 * heads * dv * 4) + align256(cols * 2 * heads * 8) + align256(cols * sizeof(JoinDesc));
 }
 
 cudaError_t launch_paged_decode(const PagedDecodeParams& p, bool fp8, const CUtensorMap* maps, void* workspace,
                                 int num_sms, cudaStream_t stream) {
-  const int cols = decode_cols(p.kv_heads, num_sms);
+  const int cols =
+      decode_cols(p.kv_heads, num_sms * ctas_per_sm(p.dq, p.dv, fp8, p.heads / p.kv_heads > 8 ? 2 : 1));
   Workspace ws = {};
   if (cols > 1) {
     uint8_t* at = static_cast<uint8_t*>(workspace);

@@ -477,17 +477,26 @@ def _stream_ptr(stream, dev):
     return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
-def _same_device(dev, *ts):
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be on the current CUDA device")
+_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
 
 
-def _token_stride(t, what, n, h, d):
+def _refuse(t, what, want):
+    raise ValueError(f"{what} must be {want} on the current CUDA device, not {t.dtype} {list(t.shape)} on {t.device}"
+                     + ("" if t.is_contiguous() else " (not contiguous)"))
+
+
+def _array(t, dev, dtype, shape, what):
+    """Pointer of a contiguous tensor of this type and shape on device dev."""
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(t, what, f"a contiguous {dtype} {list(shape)} tensor")
+    return t.data_ptr()
+
+
+def _token_stride(t, dev, n, h, d, what):
     """Token stride in elements of a bf16 [n, h, d] tensor whose heads are contiguous within a token (a part of a wider
     projection is); the stride of a single token is never used and reported as the row's length."""
-    if t.dtype is not torch.bfloat16 or t.shape != (n, h, d):
-        raise ValueError(f"{what} must be bf16 {[n, h, d]}, not {t.dtype} {list(t.shape)}")
+    if t.get_device() != dev or t.dtype is not _BF16 or t.shape != (n, h, d):
+        _refuse(t, what, f"a bf16 {[n, h, d]} tensor")
     if t.is_contiguous():
         return h * d
     st, sh, sd = t.stride()
@@ -496,20 +505,12 @@ def _token_stride(t, what, n, h, d):
     return st if n > 1 else h * d
 
 
-def _contiguous(t, what, dtype, shape):
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} tensor, not {t.dtype} {list(t.shape)}")
-
-
-def _paged_cache(k_cache, v_cache, dtype):
-    """(num_blocks, kv_heads, dq, dv) of a paged cache."""
-    nb, bl, hkv, dq = k_cache.shape
+def _paged_cache(k_cache, v_cache, dev, dtype):
+    """(num_blocks, kv_heads, dq, dv, pointers) of a paged cache."""
+    nb, _, hkv, dq = k_cache.shape
     dv = v_cache.shape[3]
-    if bl != 64:
-        raise ValueError("caches are [num_blocks, 64, kv_heads, d]")
-    _contiguous(k_cache, "k_cache", dtype, (nb, 64, hkv, dq))
-    _contiguous(v_cache, "v_cache", dtype, (nb, 64, hkv, dv))
-    return nb, hkv, dq, dv
+    return nb, hkv, dq, dv, _array(k_cache, dev, dtype, (nb, 64, hkv, dq), "k_cache"), _array(v_cache, dev, dtype,
+                                                                                            (nb, 64, hkv, dv), "v_cache")
 
 
 def _empty(shape, dtype, like, stream):
@@ -532,22 +533,18 @@ class _Scratch(threading.local):
 _scratches = _Scratch()
 
 
-def _scratch(workspace, need, like, stream, dev, raw):
-    """(tensor, pointer, bytes) of the caller's workspace, or of one of at least `need` bytes for this call."""
-    if workspace is None:
-        if need == 0:
-            return None, 0, 0
-        if stream is not None or torch.cuda.is_current_stream_capturing():
-            workspace = _empty(need, torch.uint8, like, stream)
-        else:
-            kept = _scratches.by_stream.get((dev, raw))
-            if kept is None or kept[2] < need:
-                t = torch.empty(need, dtype=torch.uint8, device=like.device)
-                kept = _scratches.by_stream[(dev, raw)] = (t, t.data_ptr(), need)
-            return kept
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+def _scratch(need, like, stream, dev, raw):
+    """(tensor, pointer, bytes) of a workspace of at least `need` bytes for one call."""
+    if need == 0:
+        return None, 0, 0
+    if stream is not None or torch.cuda.is_current_stream_capturing():
+        t = _empty(need, _U8, like, stream)
+        return t, t.data_ptr(), need
+    kept = _scratches.by_stream.get((dev, raw))
+    if kept is None or kept[2] < need:
+        t = torch.empty(need, dtype=_U8, device=like.device)
+        kept = _scratches.by_stream[(dev, raw)] = (t, t.data_ptr(), need)
+    return kept
 
 
 def _call(name, op, form, *words):
@@ -559,44 +556,50 @@ def _call(name, op, form, *words):
 def _rope_append(name, op, q, k, v, cos_sin, k_cache, v_cache, scales, block_table, cu_seqlens_q, ctx_lens, q_out, k_out,
                  rot_start, interleaved, stream):
     dev = torch.cuda.current_device()
-    _same_device(dev, q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_q, ctx_lens, q_out, k_out, *scales)
     T, Hkv, dq = k.shape
-    ks = _token_stride(k, "k", T, Hkv, dq)
+    ks = _token_stride(k, dev, T, Hkv, dq, "k")
     batch = cu_seqlens_q.shape[0] - 1
-    _contiguous(cu_seqlens_q, "cu_seqlens_q", torch.int32, (batch + 1,))
+    cu = _array(cu_seqlens_q, dev, _I32, (batch + 1,), "cu_seqlens_q")
     ctx = vp = vs = qp = qs = H = qop = qos = kop = kos = nb = mb = kc = vc = bt = rows = rot = cs = 0
     dv = 64  # no values without a cache
     if ctx_lens is not None:
-        _contiguous(ctx_lens, "ctx_lens", torch.int32, (batch,))
-        ctx = ctx_lens.data_ptr()
+        ctx = _array(ctx_lens, dev, _I32, (batch,), "ctx_lens")
     if k_cache is not None:
-        nb, kv, kd, dv = _paged_cache(k_cache, v_cache, torch.uint8 if scales else torch.bfloat16)
+        nb, kv, kd, dv, kc, vc = _paged_cache(k_cache, v_cache, dev, _U8 if scales else _BF16)
         if kv != Hkv or kd != dq:
             raise ValueError("k and the key cache have different heads or head dims")
         mb = block_table.shape[1]
-        _contiguous(block_table, "block_table", torch.int32, (batch, mb))
-        vs = _token_stride(v, "v", T, Hkv, dv)
-        vp, kc, vc, bt = v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()
+        bt = _array(block_table, dev, _I32, (batch, mb), "block_table")
+        vs = _token_stride(v, dev, T, Hkv, dv, "v")
+        vp = v.data_ptr()
     if q is not None:
         H = q.shape[1]
-        qs = _token_stride(q, "q", T, H, dq)
+        qs = _token_stride(q, dev, T, H, dq, "q")
         if q_out is None:
-            q_out = _empty((T, H, dq), torch.bfloat16, q, stream)
-        qos = _token_stride(q_out, "q_out", T, H, dq)
+            q_out = _empty((T, H, dq), _BF16, q, stream)
+        qos = _token_stride(q_out, dev, T, H, dq, "q_out")
         qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if k_out is not None:
-        kos = _token_stride(k_out, "k_out", T, Hkv, dq)
+        kos = _token_stride(k_out, dev, T, Hkv, dq, "k_out")
         kop = k_out.data_ptr()
     if cos_sin is not None:
         rows, rot = cos_sin.shape
-        _contiguous(cos_sin, "cos_sin", torch.float32, (rows, rot))
-        cs = cos_sin.data_ptr()
-    _call(name, op, _ROPE_FP8 if scales else _ROPE, qp, qs, k.data_ptr(), ks, vp, vs, cs, rows, rot_start, rot,
-          1 if interleaved else 0, qop, qos, kop, kos, kc, vc, *[s.data_ptr() for s in scales], bt, mb, nb,
-          cu_seqlens_q.data_ptr(), ctx, batch, T, H, Hkv, dq, dv, _stream_ptr(stream, dev))
+        cs = _array(cos_sin, dev, _F32, (rows, rot), "cos_sin")
+    il = 1 if interleaved else 0
+    if scales:
+        _call(name, op, _ROPE_FP8, qp, qs, k.data_ptr(), ks, vp, vs, cs, rows, rot_start, rot, il, qop, qos, kop, kos, kc, vc,
+              *scales, bt, mb, nb, cu, ctx, batch, T, H, Hkv, dq, dv, _stream_ptr(stream, dev))
+    else:
+        _call(name, op, _ROPE, qp, qs, k.data_ptr(), ks, vp, vs, cs, rows, rot_start, rot, il, qop, qos, kop, kos, kc, vc, bt,
+              mb, nb, cu, ctx, batch, T, H, Hkv, dq, dv, _stream_ptr(stream, dev))
     return q_out
+
+
+def _scale_ptrs(k_scale, v_scale, kv_heads):
+    dev = torch.cuda.current_device()
+    return _array(k_scale, dev, _F32, (kv_heads,), "k_scale"), _array(v_scale, dev, _F32, (kv_heads,), "v_scale")
 
 
 def vpp_rope_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_q, ctx_lens=None, q_out=None, k_out=None,
@@ -614,9 +617,9 @@ def vpp_rope_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_
 def vpp_rope_append_fp8(q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, ctx_lens=None,
                         q_out=None, k_out=None, rot_start=0, interleaved=False, stream=None):
     """vpp_rope_append into an E4M3 paged cache (uint8 codes, per-kv-head scales)."""
-    _scales(k_scale, v_scale, k.shape[1])
-    return _rope_append("vpp_rope_append_fp8", _OP_ROPE_FP8, q, k, v, cos_sin, k_cache, v_cache, (k_scale, v_scale), block_table,
-                        cu_seqlens_q, ctx_lens, q_out, k_out, rot_start, interleaved, stream)
+    return _rope_append("vpp_rope_append_fp8", _OP_ROPE_FP8, q, k, v, cos_sin, k_cache, v_cache,
+                        _scale_ptrs(k_scale, v_scale, k.shape[1]), block_table, cu_seqlens_q, ctx_lens, q_out, k_out, rot_start,
+                        interleaved, stream)
 
 
 @functools.lru_cache(maxsize=256)
@@ -626,25 +629,29 @@ def decode_attn_workspace_size(batch, heads, kv_heads, dq, dv):
 
 def _decode_attn(name, op, q, k_cache, v_cache, scales, block_table, ctx_lens, out, lse, softmax_scale, workspace, stream):
     dev = torch.cuda.current_device()
-    _same_device(dev, q, k_cache, v_cache, block_table, ctx_lens, out, lse, workspace, *scales)
     B, H, _ = q.shape
-    nb, Hkv, dq, dv = _paged_cache(k_cache, v_cache, torch.uint8 if scales else torch.bfloat16)
-    qs = _token_stride(q, "q", B, H, dq)
+    nb, Hkv, dq, dv, kc, vc = _paged_cache(k_cache, v_cache, dev, _U8 if scales else _BF16)
+    qs = _token_stride(q, dev, B, H, dq, "q")
     mb = block_table.shape[1]
-    _contiguous(block_table, "block_table", torch.int32, (B, mb))
-    _contiguous(ctx_lens, "ctx_lens", torch.int32, (B,))
+    bt = _array(block_table, dev, _I32, (B, mb), "block_table")
+    ctx = _array(ctx_lens, dev, _I32, (B,), "ctx_lens")
     if out is None:
-        out = _empty((B, H, dv), torch.bfloat16, q, stream)
-    else:
-        _contiguous(out, "out", torch.bfloat16, (B, H, dv))
-    if lse is not None:
-        _contiguous(lse, "lse", torch.float32, (H, B))
+        out = _empty((B, H, dv), _BF16, q, stream)
+    op_ = _array(out, dev, _BF16, (B, H, dv), "out")
+    lp = 0 if lse is None else _array(lse, dev, _F32, (H, B), "lse")
     raw = _stream_ptr(stream, dev)
-    need = decode_attn_workspace_size(B, H, Hkv, dq, dv) if workspace is None else 0
-    workspace, wp, wb = _scratch(workspace, need, q, stream, dev, raw)
-    _call(name, op, _DECODE_FP8 if scales else _DECODE, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(),
-          *[s.data_ptr() for s in scales], block_table.data_ptr(), mb, nb, ctx_lens.data_ptr(), B, H, Hkv, dq, dv,
-          softmax_scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(), wp, wb, raw)
+    if workspace is None:
+        workspace, wp, wb = _scratch(decode_attn_workspace_size(B, H, Hkv, dq, dv), q, stream, dev, raw)
+    else:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            _refuse(workspace, "workspace", "contiguous")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if scales:
+        _call(name, op, _DECODE_FP8, q.data_ptr(), qs, kc, vc, *scales, bt, mb, nb, ctx, B, H, Hkv, dq, dv, softmax_scale, op_,
+              lp, wp, wb, raw)
+    else:
+        _call(name, op, _DECODE, q.data_ptr(), qs, kc, vc, bt, mb, nb, ctx, B, H, Hkv, dq, dv, softmax_scale, op_, lp, wp, wb,
+              raw)
     return out
 
 
@@ -662,9 +669,9 @@ def vpp_decode_attn(q, k_cache, v_cache, block_table, ctx_lens, out=None, lse=No
 def vpp_decode_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out=None, lse=None, softmax_scale=0.0,
                         workspace=None, stream=None):
     """vpp_decode_attn over an E4M3 paged cache (uint8 codes, per-kv-head scales)."""
-    _scales(k_scale, v_scale, k_cache.shape[2])
-    return _decode_attn("vpp_decode_attn_fp8", _OP_DECODE_FP8, q, k_cache, v_cache, (k_scale, v_scale), block_table, ctx_lens,
-                        out, lse, softmax_scale, workspace, stream)
+    return _decode_attn("vpp_decode_attn_fp8", _OP_DECODE_FP8, q, k_cache, v_cache,
+                        _scale_ptrs(k_scale, v_scale, k_cache.shape[2]), block_table, ctx_lens, out, lse, softmax_scale,
+                        workspace, stream)
 
 
 def vpp_prompt_attn(q, k, v, cu_seqlens, out=None, lse=None, softmax_scale=0.0, stream=None):
@@ -672,23 +679,19 @@ def vpp_prompt_attn(q, k, v, cu_seqlens, out=None, lse=None, softmax_scale=0.0, 
     bf16 [tokens, heads, d], contiguous or parts of one fused projection);
     cu_seqlens (int32 CUDA tensor) is read when the kernel runs."""
     dev = torch.cuda.current_device()
-    _same_device(dev, q, k, v, cu_seqlens, out, lse)
     T, H, dq = q.shape
     _, Hkv, dv = v.shape
-    qs = _token_stride(q, "q", T, H, dq)
-    ks = _token_stride(k, "k", T, Hkv, dq)
-    vs = _token_stride(v, "v", T, Hkv, dv)
+    qs = _token_stride(q, dev, T, H, dq, "q")
+    ks = _token_stride(k, dev, T, Hkv, dq, "k")
+    vs = _token_stride(v, dev, T, Hkv, dv, "v")
     batch = cu_seqlens.shape[0] - 1
-    _contiguous(cu_seqlens, "cu_seqlens", torch.int32, (batch + 1,))
+    cu = _array(cu_seqlens, dev, _I32, (batch + 1,), "cu_seqlens")
     if out is None:
-        out = _empty((T, H, dv), torch.bfloat16, q, stream)
-    else:
-        _contiguous(out, "out", torch.bfloat16, (T, H, dv))
-    if lse is not None:
-        _contiguous(lse, "lse", torch.float32, (H, T))
-    _call("vpp_prompt_attn", _OP_PROMPT, _PROMPT, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu_seqlens.data_ptr(),
-          batch, T, H, Hkv, dq, dv, softmax_scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
-          _stream_ptr(stream, dev))
+        out = _empty((T, H, dv), _BF16, q, stream)
+    op_ = _array(out, dev, _BF16, (T, H, dv), "out")
+    lp = 0 if lse is None else _array(lse, dev, _F32, (H, T), "lse")
+    _call("vpp_prompt_attn", _OP_PROMPT, _PROMPT, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu, batch, T, H, Hkv,
+          dq, dv, softmax_scale, op_, lp, _stream_ptr(stream, dev))
     return out
 
 
