@@ -252,3 +252,74 @@ def test_offsets_past_32_bits():
     out = call(False, q.to(DEV), kc, vc, None, None, table.to(DEV), ctx, lse=lse)
     assert vpp.vpp_last_device_status() == 0
     check_rows(out, lse, q, keys, vals, ctx, d, False)
+
+
+def test_captured_and_eager_calls_without_a_workspace_do_not_share_one():
+    """A captured call that was given no workspace is replayed on one stream while eager calls run on another and on the
+    stream of the capture."""
+    H, Hkv, d = 16, 4, 128
+    ctx = [4000, 50, 1700]
+    kc, vc, ks, vs, table, _, _ = make(ctx, Hkv, d, d, False)
+    lens = torch.tensor(ctx, dtype=torch.int32, device=DEV)
+    qa, qb = randn((3, H, d), 60).to(DEV), randn((3, H, d), 61).to(DEV)
+    want_a, want_b = call(False, qa, kc, vc, ks, vs, table, lens), call(False, qb, kc, vc, ks, vs, table, lens)
+    out = torch.empty_like(want_a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(False, qa, kc, vc, ks, vs, table, lens, out=out)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(30):
+        with torch.cuda.stream(side):
+            graph.replay()
+        got.append(call(False, qb, kc, vc, ks, vs, table, lens))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want_a)
+    assert all(torch.equal(o, want_b) for o in got)
+
+
+def test_threads_on_one_stream():
+    """Several host threads call on the same stream: a call is two launches, and each thread has its own workspace."""
+    import threading
+
+    H, Hkv, d = 16, 4, 128
+    ctx = [4000, 50, 1700]
+    kc, vc, ks, vs, table, _, _ = make(ctx, Hkv, d, d, False)
+    lens = torch.tensor(ctx, dtype=torch.int32, device=DEV)
+    qs = [randn((3, H, d), 70 + i).to(DEV) for i in range(4)]
+    want = [call(False, q, kc, vc, ks, vs, table, lens) for q in qs]
+    got = [[] for _ in qs]
+
+    def work(i):
+        for _ in range(50):
+            got[i].append(call(False, qs[i], kc, vc, ks, vs, table, lens))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+def test_infinite_scores():
+    """A row whose scores are all -inf has weights that sum to nothing (0 and -inf, as an empty row); a NaN key gives NaN
+    to the heads that read it and to no other row."""
+    H, Hkv, d = 4, 2, 64
+    ctx = [40, 40, 40]
+    kc, vc, ks, vs, table, keys, vals = make(ctx, Hkv, d, d, False)
+    q = torch.ones((3, H, d), dtype=torch.bfloat16)
+    host = kc.cpu()
+    keys[0][:, 0] = float("-inf")
+    keys[1][7, 1] = float("nan")
+    for b in (0, 1):
+        fill_cache(host, table.cpu(), b, keys[b])
+    lse = torch.empty((H, 3), device=DEV)
+    out = call(False, q.to(DEV), host.to(DEV), vc, ks, vs, table, ctx, lse=lse).float().cpu()
+    assert not bool(out[0, :2].any()) and bool((lse[:2, 0] == -math.inf).all())
+    assert bool(out[1, 2:].isnan().all()) and bool(lse[2:, 1].isnan().all())
+    assert bool(out[0, 2:].isfinite().all()) and bool(out[1, :2].isfinite().all()) and bool(out[2].isfinite().all())

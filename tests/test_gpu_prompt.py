@@ -37,9 +37,11 @@ SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("H,Hkv,dq,dv", SHAPES)
-def test_matches_formula(H, Hkv, dq, dv):
-    cu = starts(LENS)
+# LENS runs with one query tile a CTA in most shapes, four times LENS with pairs of tiles.
+@pytest.mark.parametrize("times", [1, 4])
+@pytest.mark.parametrize("H,Hkv,dq,dv", SHAPES + [(32, 8, 128, 128), (24, 8, 64, 128)])
+def test_matches_formula(H, Hkv, dq, dv, times):
+    cu = starts(LENS * times)
     T = int(cu[-1]) + 5
     x = randn((T, H * dq + Hkv * (dq + dv)), 1)
     q, k, v = views(x, H, Hkv, dq, dv)
@@ -63,7 +65,7 @@ def test_batch_shapes(lens):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-@pytest.mark.parametrize("H,Hkv,d", [(8, 2, 128), (6, 2, 64), (2, 2, 128)])
+@pytest.mark.parametrize("H,Hkv,d", [(8, 2, 128), (6, 2, 64), (2, 2, 128), (32, 8, 128), (48, 16, 64)])
 def test_neighbours_never_reach_a_result(H, Hkv, d, bad):
     """Sequences of hostile values before and behind each good one, and in the rows of no sequence."""
     lens = [30, 100, 40, 129, 10, 200, 3]
@@ -171,3 +173,48 @@ def test_another_stream():
     got = [vpp.vpp_prompt_attn(q, k, v, cud, stream=s) for _ in range(10) for s in streams]
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in got)
+
+
+def test_many_ragged_sequences():
+    """More sequences than the work list keeps in registers, of very different lengths, empty ones among them."""
+    H, Hkv, d = 8, 4, 64
+    g = torch.Generator().manual_seed(30)
+    lens = [int(x) for x in (torch.rand(900, generator=g) ** 6 * 500).long()]
+    lens[17], lens[600], lens[899] = 900, 0, 333
+    cu = starts(lens)
+    T = int(cu[-1])
+    q, k, v = randn((T, H, d), 31), randn((T, Hkv, d), 32), randn((T, Hkv, d), 33)
+    lse = torch.full((H, T), 7.0, device=DEV)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    check_sequences(out, lse, q, k, v, cu, d)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(8, 8, 128), (32, 8, 64)])
+def test_few_live_rows_of_many(H, Hkv, d):
+    """A launch sized for many rows of which almost none belong to a sequence."""
+    T = 20000
+    q, k, v = (torch.full((T, h, d), float("nan"), dtype=torch.bfloat16, device=DEV) for h in (H, Hkv, Hkv))
+    live = [randn((70, h, d), 34 + h) for h in (H, Hkv, Hkv)]
+    for x, y in zip((q, k, v), live):
+        x[5:75] = y.to(DEV)
+    cu = torch.tensor([5, 5, 75, 75], dtype=torch.int32)
+    out = torch.full((T, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    vpp.vpp_prompt_attn(q, k, v, cu.to(DEV), out=out)
+    check_sequences(out[5:75], None, *live, [0, 70], d)
+    assert bool((out[:5] == 7).all()) and bool((out[75:] == 7).all())
+    assert vpp.vpp_last_device_status() == 0
+
+
+def test_growing_scores_rescale():
+    """Keys whose scores grow along a long sequence, so that the running maximum moves on nearly every tile."""
+    H, Hkv, d, n = 32, 8, 128, 1300
+    base = randn((H, d), 40).float()
+    ramp = torch.linspace(0.2, 3, n)
+    q = base[None].expand(n, H, d).to(torch.bfloat16)
+    k = (ramp[:, None, None] * base[:: H // Hkv][None]).to(torch.bfloat16)
+    v = randn((n, Hkv, d), 41)
+    cu = starts([n])
+    lse = torch.empty((H, n), device=DEV)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse, softmax_scale=0.2)
+    check_sequences(out, lse, q, k, v, cu, d, scale=0.2)
