@@ -500,7 +500,9 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
               if (!ok) break;
             }
             if (j > 0) {
-              const bool adjacent = S::NVC == 1 || vslot + S::NVC <= S::NSLOT;
+              // (V tiles of two slots never wrap when everything comes in twos)
+              constexpr bool kTwos = S::NQC % 2 == 0 && S::NVC == 2 && S::NSLOT % 2 == 0;
+              const bool adjacent = S::NVC == 1 || kTwos || vslot + S::NVC <= S::NSLOT;
               auto pv_steps = [&](int k0, int k1) {
                 if (adjacent) {
                   const uint64_t vb = dv0 + vslot * kSub16;
