@@ -1,5 +1,6 @@
 """Builds libvpp.so (sm_103a) in-tree: one nvcc -c per .cu file, in parallel,
-then one shared-library link with the CUDA runtime linked statically."""
+then one shared-library link with the CUDA runtime linked statically; and the
+binding's call module (csrc/pycall.c)."""
 
 from __future__ import annotations
 
@@ -8,6 +9,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -39,6 +41,20 @@ def _stale(obj, src, hdr_mtime):
             or os.path.getmtime(obj) < hdr_mtime)
 
 
+def _call_module(out):
+    """Compiles csrc/pycall.c, the argument marshalling of the serving-step calls (a CPython extension module, host code
+    only), and returns its path."""
+    src, so = os.path.join(CSRC, "pycall.c"), os.path.join(out, "_vppcall.so")
+    if _stale(so, src, os.path.getmtime(os.path.join(INCLUDE, "vpp.h"))):
+        cmd = [os.environ.get("CC", "gcc"), "-O2", "-fPIC", "-shared", "-Wall", "-I" + INCLUDE,
+               "-I" + sysconfig.get_paths()["include"], src, "-o", so + ".tmp"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"compiling pycall.c failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(so + ".tmp", so)
+    return so
+
+
 def build(verbose: bool = False, jobs: int | None = None, extra_flags=(), out_dir: str | None = None,
           lib_name: str = "libvpp.so") -> str:
     """Compiles what changed and (re)links the library; returns its path.
@@ -49,6 +65,7 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=(), out_di
     out = out_dir or OUT_DIR
     lib = os.path.join(out, lib_name)
     os.makedirs(out, exist_ok=True)
+    _call_module(out)
     nvcc = _nvcc()
     hdr_mtime = max((os.path.getmtime(h) for h in _headers()), default=0.0)
     srcs = _sources()

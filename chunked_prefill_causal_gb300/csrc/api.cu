@@ -1363,140 +1363,6 @@ int vpp_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_st
              : VPP_ERR_CUDA;
 }
 
-}  // extern "C"
-
-namespace {
-
-// The words of a vpp_call: every accessor takes the next one.
-struct Words {
-  const uint8_t* at;
-  bool ok = true;
-  int64_t word() {
-    int64_t w;
-    std::memcpy(&w, at, 8);
-    at += 8;
-    return w;
-  }
-  int32_t i32() {
-    const int64_t w = word();
-    if (w < INT32_MIN || w > INT32_MAX) ok = false;
-    return static_cast<int32_t>(w);
-  }
-  float f32() {
-    float f;
-    std::memcpy(&f, at, 4);
-    at += 8;
-    return f;
-  }
-  template <typename T>
-  T* ptr() {
-    return reinterpret_cast<T*>(static_cast<uintptr_t>(word()));
-  }
-};
-
-int call_rope(Words w, bool fp8) {
-  RopeParams p = {};
-  p.q = w.ptr<const uint16_t>();
-  p.q_stride = w.word();
-  p.k = w.ptr<const uint16_t>();
-  p.k_stride = w.word();
-  p.v = w.ptr<const uint16_t>();
-  p.v_stride = w.word();
-  p.cos_sin = w.ptr<const float>();
-  p.table_rows = w.i32();
-  p.rot_start = w.i32();
-  p.rot_dim = w.i32();
-  const int interleaved = w.i32();
-  p.q_out = w.ptr<uint16_t>();
-  p.q_out_stride = w.word();
-  p.k_out = w.ptr<uint16_t>();
-  p.k_out_stride = w.word();
-  p.k_cache = w.ptr<void>();
-  p.v_cache = w.ptr<void>();
-  if (fp8) {
-    p.k_scale = w.ptr<const float>();
-    p.v_scale = w.ptr<const float>();
-  }
-  p.block_table = w.ptr<const int32_t>();
-  p.max_blocks_per_seq = w.i32();
-  p.num_blocks = w.i32();
-  p.cu = w.ptr<const int32_t>();
-  p.ctx = w.ptr<const int32_t>();
-  p.batch = w.i32();
-  p.total_q = w.word();
-  p.heads = w.i32();
-  p.kv_heads = w.i32();
-  p.dq = w.i32();
-  p.dv = w.i32();
-  void* stream = w.ptr<void>();
-  return w.ok ? rope_append_impl(fp8, p, interleaved, as_stream(stream)) : VPP_ERR_INVALID;
-}
-
-int call_decode(Words w, bool fp8) {
-  PagedDecodeParams p = {};
-  p.q = w.ptr<const uint16_t>();
-  p.q_stride = w.word();
-  p.k_cache = w.ptr<const void>();
-  p.v_cache = w.ptr<const void>();
-  if (fp8) {
-    p.k_scale = w.ptr<const float>();
-    p.v_scale = w.ptr<const float>();
-  }
-  p.block_table = w.ptr<const int32_t>();
-  p.max_blocks_per_seq = w.i32();
-  p.num_blocks = w.i32();
-  p.ctx = w.ptr<const int32_t>();
-  p.batch = w.i32();
-  p.heads = w.i32();
-  p.kv_heads = w.i32();
-  p.dq = w.i32();
-  p.dv = w.i32();
-  const float scale = w.f32();
-  p.out = w.ptr<uint16_t>();
-  p.lse = w.ptr<float>();
-  void* workspace = w.ptr<void>();
-  const int64_t bytes = w.word();
-  void* stream = w.ptr<void>();
-  if (!w.ok || bytes < 0) return VPP_ERR_INVALID;
-  return decode_attn_impl(fp8, p, scale, workspace, static_cast<size_t>(bytes), as_stream(stream));
-}
-
-int call_prompt(Words w) {
-  const void* q = w.ptr<const void>();
-  const int64_t qs = w.word();
-  const void* k = w.ptr<const void>();
-  const int64_t ks = w.word();
-  const void* v = w.ptr<const void>();
-  const int64_t vs = w.word();
-  const int32_t* cu = w.ptr<const int32_t>();
-  const int32_t batch = w.i32();
-  const int64_t total = w.word();
-  const int heads = w.i32(), kv_heads = w.i32(), dq = w.i32(), dv = w.i32();
-  const float scale = w.f32();
-  void* out = w.ptr<void>();
-  float* lse = w.ptr<float>();
-  void* stream = w.ptr<void>();
-  if (!w.ok) return VPP_ERR_INVALID;
-  return vpp_prompt_attn(q, qs, k, ks, v, vs, cu, batch, total, heads, kv_heads, dq, dv, scale, out, lse, stream);
-}
-
-}  // namespace
-
-extern "C" {
-
-int vpp_call(int op, const void* args, int nargs) {
-  if (!args) return VPP_ERR_INVALID;
-  const Words w{static_cast<const uint8_t*>(args)};
-  switch (op) {
-    case VPP_CALL_ROPE_APPEND: return nargs == 29 ? call_rope(w, false) : VPP_ERR_INVALID;
-    case VPP_CALL_ROPE_APPEND_FP8: return nargs == 31 ? call_rope(w, true) : VPP_ERR_INVALID;
-    case VPP_CALL_DECODE_ATTN: return nargs == 19 ? call_decode(w, false) : VPP_ERR_INVALID;
-    case VPP_CALL_DECODE_ATTN_FP8: return nargs == 21 ? call_decode(w, true) : VPP_ERR_INVALID;
-    case VPP_CALL_PROMPT_ATTN: return nargs == 17 ? call_prompt(w) : VPP_ERR_INVALID;
-    default: return VPP_ERR_INVALID;
-  }
-}
-
 int vpp_last_device_status(void* stream, int* code) {
   if (!code) return VPP_ERR_INVALID;
   DeviceState* ds = nullptr;

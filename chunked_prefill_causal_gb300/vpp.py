@@ -9,9 +9,9 @@ in the library's CUDA kernels; there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
-import struct
 import threading
 
 import torch
@@ -80,7 +80,6 @@ SIGNATURES = {
     "vpp_decode_attn_workspace_size": ([_i32, _int, _int, _int, _int], _sz),
     "vpp_prompt_attn": ([_c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i64, _c_void_p, _i32, _i64, _int, _int, _int, _int,
                          _f32, _c_void_p, _c_void_p, _c_void_p], _int),
-    "vpp_call": ([_int, ctypes.c_char_p, _int], _int),
     "vpp_last_device_status": ([_c_void_p, ctypes.POINTER(_int)], _int),
     "vpp_selftest_wait_timeout": ([_int, _c_void_p], _int),
 }
@@ -462,12 +461,28 @@ def vpp_topk_chunk_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_len, t
 
 
 # ----------------------------------------------------------------- lengths on the device
-# These calls are a few microseconds of GPU time at decode sizes, so their
-# arguments travel as one packed array of 64-bit words (vpp_call): converting
-# thirty ctypes arguments one by one takes longer than the smallest kernels.
-_OP_ROPE, _OP_ROPE_FP8, _OP_DECODE, _OP_DECODE_FP8, _OP_PROMPT = 1, 2, 3, 4, 5
-_ROPE, _ROPE_FP8 = struct.Struct("=29q"), struct.Struct("=31q")
-_DECODE, _DECODE_FP8, _PROMPT = struct.Struct("=13qf4x5q"), struct.Struct("=15qf4x5q"), struct.Struct("=13qf4x3q")
+# These calls are a few microseconds of GPU time at decode sizes: their arguments
+# are checked and passed on by a compiled module (csrc/pycall.c).
+CALL_PATH = os.path.join(_HERE, "_build", "_vppcall.so")
+_call_module = None
+
+
+def _calls():
+    global _call_module
+    if _call_module is None:
+        lib = load()
+        if not os.path.exists(CALL_PATH):
+            raise RuntimeError(f"{CALL_PATH} not found: run __graft_entry__.build() first")
+        loader = importlib.machinery.ExtensionFileLoader("_vppcall", CALL_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_vppcall", loader))
+        loader.exec_module(module)
+        names = ("vpp_rope_append", "vpp_rope_append_fp8", "vpp_decode_attn", "vpp_decode_attn_fp8", "vpp_prompt_attn")
+        module.setup((torch.bfloat16, torch.float32, torch.int32, torch.uint8),
+                     tuple(ctypes.cast(getattr(lib, n), _c_void_p).value for n in names))
+        _call_module = module
+    return _call_module
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -477,48 +492,49 @@ def _stream_ptr(stream, dev):
     return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
-_BF16, _F32, _I32, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
-
-
-def _refuse(t, what, want):
-    raise ValueError(f"{what} must be {want} on the current CUDA device, not {t.dtype} {list(t.shape)} on {t.device}"
-                     + ("" if t.is_contiguous() else " (not contiguous)"))
-
-
-def _array(t, dev, dtype, shape, what):
-    """Pointer of a contiguous tensor of this type and shape on device dev."""
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(t, what, f"a contiguous {dtype} {list(shape)} tensor")
-    return t.data_ptr()
-
-
-def _token_stride(t, dev, n, h, d, what):
-    """Token stride in elements of a bf16 [n, h, d] tensor whose heads are contiguous within a token (a part of a wider
-    projection is); the stride of a single token is never used and reported as the row's length."""
-    if t.get_device() != dev or t.dtype is not _BF16 or t.shape != (n, h, d):
-        _refuse(t, what, f"a bf16 {[n, h, d]} tensor")
-    if t.is_contiguous():
-        return h * d
-    st, sh, sd = t.stride()
-    if (sd != 1 and d > 1) or (sh != d and h > 1):
-        raise ValueError(f"{what}: a token's heads must be contiguous")
-    return st if n > 1 else h * d
-
-
-def _paged_cache(k_cache, v_cache, dev, dtype):
-    """(num_blocks, kv_heads, dq, dv, pointers) of a paged cache."""
-    nb, _, hkv, dq = k_cache.shape
-    dv = v_cache.shape[3]
-    return nb, hkv, dq, dv, _array(k_cache, dev, dtype, (nb, 64, hkv, dq), "k_cache"), _array(v_cache, dev, dtype,
-                                                                                            (nb, 64, hkv, dv), "v_cache")
-
-
 def _empty(shape, dtype, like, stream):
     """A tensor for a kernel on `stream` (the current one when None) to write."""
     t = torch.empty(shape, dtype=dtype, device=like.device)
     if stream is not None:
         t.record_stream(stream)
     return t
+
+
+def _rope_append(name, q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, ctx_lens, q_out, k_out,
+                 rot_start, interleaved, stream):
+    if q is not None and q_out is None:
+        q_out = _empty(q.shape, torch.bfloat16, q, stream)
+    dev = torch.cuda.current_device()
+    code = _calls().rope(dev, _stream_ptr(stream, dev), q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table,
+                         cu_seqlens_q, ctx_lens, q_out, k_out, rot_start, interleaved)
+    if code != VPP_OK:
+        raise VppError(name, code)
+    return q_out
+
+
+def vpp_rope_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_q, ctx_lens=None, q_out=None, k_out=None,
+                    rot_start=0, interleaved=False, stream=None):
+    """Rotate new queries and keys by their positions (row n of cos_sin for
+    position n) and append keys and values to a bf16 paged cache; returns
+    q_out.  q, k, v: bf16 [tokens, heads, d], contiguous or parts of one fused
+    projection.  cu_seqlens_q, ctx_lens: int32 CUDA tensors, read when the
+    kernel runs.  q_out / k_out may be q / k themselves (rotation in place);
+    q None rotates keys only; caches, v and block_table None rotate only."""
+    return _rope_append("vpp_rope_append", q, k, v, cos_sin, k_cache, v_cache, None, None, block_table, cu_seqlens_q, ctx_lens,
+                        q_out, k_out, rot_start, interleaved, stream)
+
+
+def vpp_rope_append_fp8(q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, ctx_lens=None,
+                        q_out=None, k_out=None, rot_start=0, interleaved=False, stream=None):
+    """vpp_rope_append into an E4M3 paged cache (uint8 codes, per-kv-head scales)."""
+    if k_cache is None or k_scale is None:
+        raise ValueError("the caches and their scales are required")
+    return _rope_append("vpp_rope_append_fp8", q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q,
+                        ctx_lens, q_out, k_out, rot_start, interleaved, stream)
+
+
+def decode_attn_workspace_size(batch, heads, kv_heads, dq, dv):
+    return int(load().vpp_decode_attn_workspace_size(int(batch), heads, kv_heads, dq, dv))
 
 
 class _Scratch(threading.local):
@@ -533,125 +549,33 @@ class _Scratch(threading.local):
 _scratches = _Scratch()
 
 
-def _scratch(need, like, stream, dev, raw):
-    """(tensor, pointer, bytes) of a workspace of at least `need` bytes for one call."""
-    if need == 0:
-        return None, 0, 0
-    if stream is not None or torch.cuda.is_current_stream_capturing():
-        t = _empty(need, _U8, like, stream)
-        return t, t.data_ptr(), need
-    kept = _scratches.by_stream.get((dev, raw))
-    if kept is None or kept[2] < need:
-        t = torch.empty(need, dtype=_U8, device=like.device)
-        kept = _scratches.by_stream[(dev, raw)] = (t, t.data_ptr(), need)
-    return kept
-
-
-def _call(name, op, form, *words):
-    code = load().vpp_call(op, form.pack(*words), len(words))
+def _decode_attn(name, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse, softmax_scale, workspace, stream):
+    dev = torch.cuda.current_device()
+    raw = _stream_ptr(stream, dev)
+    if out is None:
+        out = _empty((q.shape[0], q.shape[1], v_cache.shape[3]), torch.bfloat16, q, stream)
+    own = None
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the current CUDA device")
+        ws = workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif stream is None and not torch.cuda.is_current_stream_capturing():
+        own = dev, raw
+        ws = _scratches.by_stream.get(own) or (None, 0, 0)
+    else:
+        need = decode_attn_workspace_size(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], v_cache.shape[3])
+        t = _empty(max(need, 16), torch.uint8, q, stream)
+        ws = t, t.data_ptr(), need
+    decode = _calls().decode
+    code = decode(dev, raw, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse, softmax_scale, ws[1], ws[2])
+    if code == VPP_ERR_WORKSPACE and own:
+        need = decode_attn_workspace_size(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], v_cache.shape[3])
+        t = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _scratches.by_stream[own] = t, t.data_ptr(), need
+        code = decode(dev, raw, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse, softmax_scale, ws[1],
+                      ws[2])
     if code != VPP_OK:
         raise VppError(name, code)
-
-
-def _rope_append(name, op, q, k, v, cos_sin, k_cache, v_cache, scales, block_table, cu_seqlens_q, ctx_lens, q_out, k_out,
-                 rot_start, interleaved, stream):
-    dev = torch.cuda.current_device()
-    T, Hkv, dq = k.shape
-    ks = _token_stride(k, dev, T, Hkv, dq, "k")
-    batch = cu_seqlens_q.shape[0] - 1
-    cu = _array(cu_seqlens_q, dev, _I32, (batch + 1,), "cu_seqlens_q")
-    ctx = vp = vs = qp = qs = H = qop = qos = kop = kos = nb = mb = kc = vc = bt = rows = rot = cs = 0
-    dv = 64  # no values without a cache
-    if ctx_lens is not None:
-        ctx = _array(ctx_lens, dev, _I32, (batch,), "ctx_lens")
-    if k_cache is not None:
-        nb, kv, kd, dv, kc, vc = _paged_cache(k_cache, v_cache, dev, _U8 if scales else _BF16)
-        if kv != Hkv or kd != dq:
-            raise ValueError("k and the key cache have different heads or head dims")
-        mb = block_table.shape[1]
-        bt = _array(block_table, dev, _I32, (batch, mb), "block_table")
-        vs = _token_stride(v, dev, T, Hkv, dv, "v")
-        vp = v.data_ptr()
-    if q is not None:
-        H = q.shape[1]
-        qs = _token_stride(q, dev, T, H, dq, "q")
-        if q_out is None:
-            q_out = _empty((T, H, dq), _BF16, q, stream)
-        qos = _token_stride(q_out, dev, T, H, dq, "q_out")
-        qp, qop = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if k_out is not None:
-        kos = _token_stride(k_out, dev, T, Hkv, dq, "k_out")
-        kop = k_out.data_ptr()
-    if cos_sin is not None:
-        rows, rot = cos_sin.shape
-        cs = _array(cos_sin, dev, _F32, (rows, rot), "cos_sin")
-    il = 1 if interleaved else 0
-    if scales:
-        _call(name, op, _ROPE_FP8, qp, qs, k.data_ptr(), ks, vp, vs, cs, rows, rot_start, rot, il, qop, qos, kop, kos, kc, vc,
-              *scales, bt, mb, nb, cu, ctx, batch, T, H, Hkv, dq, dv, _stream_ptr(stream, dev))
-    else:
-        _call(name, op, _ROPE, qp, qs, k.data_ptr(), ks, vp, vs, cs, rows, rot_start, rot, il, qop, qos, kop, kos, kc, vc, bt,
-              mb, nb, cu, ctx, batch, T, H, Hkv, dq, dv, _stream_ptr(stream, dev))
-    return q_out
-
-
-def _scale_ptrs(k_scale, v_scale, kv_heads):
-    dev = torch.cuda.current_device()
-    return _array(k_scale, dev, _F32, (kv_heads,), "k_scale"), _array(v_scale, dev, _F32, (kv_heads,), "v_scale")
-
-
-def vpp_rope_append(q, k, v, cos_sin, k_cache, v_cache, block_table, cu_seqlens_q, ctx_lens=None, q_out=None, k_out=None,
-                    rot_start=0, interleaved=False, stream=None):
-    """Rotate new queries and keys by their positions (row n of cos_sin for
-    position n) and append keys and values to a bf16 paged cache; returns
-    q_out.  q, k, v: bf16 [tokens, heads, d], contiguous or parts of one fused
-    projection.  cu_seqlens_q, ctx_lens: int32 CUDA tensors, read when the
-    kernel runs.  q_out / k_out may be q / k themselves (rotation in place);
-    q None rotates keys only; caches, v and block_table None rotate only."""
-    return _rope_append("vpp_rope_append", _OP_ROPE, q, k, v, cos_sin, k_cache, v_cache, (), block_table, cu_seqlens_q, ctx_lens,
-                        q_out, k_out, rot_start, interleaved, stream)
-
-
-def vpp_rope_append_fp8(q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, ctx_lens=None,
-                        q_out=None, k_out=None, rot_start=0, interleaved=False, stream=None):
-    """vpp_rope_append into an E4M3 paged cache (uint8 codes, per-kv-head scales)."""
-    return _rope_append("vpp_rope_append_fp8", _OP_ROPE_FP8, q, k, v, cos_sin, k_cache, v_cache,
-                        _scale_ptrs(k_scale, v_scale, k.shape[1]), block_table, cu_seqlens_q, ctx_lens, q_out, k_out, rot_start,
-                        interleaved, stream)
-
-
-@functools.lru_cache(maxsize=256)
-def decode_attn_workspace_size(batch, heads, kv_heads, dq, dv):
-    return int(load().vpp_decode_attn_workspace_size(int(batch), heads, kv_heads, dq, dv))
-
-
-def _decode_attn(name, op, q, k_cache, v_cache, scales, block_table, ctx_lens, out, lse, softmax_scale, workspace, stream):
-    dev = torch.cuda.current_device()
-    B, H, _ = q.shape
-    nb, Hkv, dq, dv, kc, vc = _paged_cache(k_cache, v_cache, dev, _U8 if scales else _BF16)
-    qs = _token_stride(q, dev, B, H, dq, "q")
-    mb = block_table.shape[1]
-    bt = _array(block_table, dev, _I32, (B, mb), "block_table")
-    ctx = _array(ctx_lens, dev, _I32, (B,), "ctx_lens")
-    if out is None:
-        out = _empty((B, H, dv), _BF16, q, stream)
-    op_ = _array(out, dev, _BF16, (B, H, dv), "out")
-    lp = 0 if lse is None else _array(lse, dev, _F32, (H, B), "lse")
-    raw = _stream_ptr(stream, dev)
-    if workspace is None:
-        workspace, wp, wb = _scratch(decode_attn_workspace_size(B, H, Hkv, dq, dv), q, stream, dev, raw)
-    else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            _refuse(workspace, "workspace", "contiguous")
-        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    if scales:
-        _call(name, op, _DECODE_FP8, q.data_ptr(), qs, kc, vc, *scales, bt, mb, nb, ctx, B, H, Hkv, dq, dv, softmax_scale, op_,
-              lp, wp, wb, raw)
-    else:
-        _call(name, op, _DECODE, q.data_ptr(), qs, kc, vc, bt, mb, nb, ctx, B, H, Hkv, dq, dv, softmax_scale, op_, lp, wp, wb,
-              raw)
     return out
 
 
@@ -662,36 +586,29 @@ def vpp_decode_attn(q, k_cache, v_cache, block_table, ctx_lens, out=None, lse=No
     runs, and a row of length 0 gives out = 0, lse = -inf.  Without a
     workspace the calls of a thread on the current stream share one; calls
     under capture or on a given stream allocate their own."""
-    return _decode_attn("vpp_decode_attn", _OP_DECODE, q, k_cache, v_cache, (), block_table, ctx_lens, out, lse, softmax_scale,
+    return _decode_attn("vpp_decode_attn", q, k_cache, v_cache, None, None, block_table, ctx_lens, out, lse, softmax_scale,
                         workspace, stream)
 
 
 def vpp_decode_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out=None, lse=None, softmax_scale=0.0,
                         workspace=None, stream=None):
     """vpp_decode_attn over an E4M3 paged cache (uint8 codes, per-kv-head scales)."""
-    return _decode_attn("vpp_decode_attn_fp8", _OP_DECODE_FP8, q, k_cache, v_cache,
-                        _scale_ptrs(k_scale, v_scale, k_cache.shape[2]), block_table, ctx_lens, out, lse, softmax_scale,
-                        workspace, stream)
+    if k_scale is None:
+        raise ValueError("the scales are required")
+    return _decode_attn("vpp_decode_attn_fp8", q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_lens, out, lse,
+                        softmax_scale, workspace, stream)
 
 
 def vpp_prompt_attn(q, k, v, cu_seqlens, out=None, lse=None, softmax_scale=0.0, stream=None):
     """Causal attention of whole prompts packed one after the other (q, k, v
     bf16 [tokens, heads, d], contiguous or parts of one fused projection);
     cu_seqlens (int32 CUDA tensor) is read when the kernel runs."""
-    dev = torch.cuda.current_device()
-    T, H, dq = q.shape
-    _, Hkv, dv = v.shape
-    qs = _token_stride(q, dev, T, H, dq, "q")
-    ks = _token_stride(k, dev, T, Hkv, dq, "k")
-    vs = _token_stride(v, dev, T, Hkv, dv, "v")
-    batch = cu_seqlens.shape[0] - 1
-    cu = _array(cu_seqlens, dev, _I32, (batch + 1,), "cu_seqlens")
     if out is None:
-        out = _empty((T, H, dv), _BF16, q, stream)
-    op_ = _array(out, dev, _BF16, (T, H, dv), "out")
-    lp = 0 if lse is None else _array(lse, dev, _F32, (H, T), "lse")
-    _call("vpp_prompt_attn", _OP_PROMPT, _PROMPT, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, cu, batch, T, H, Hkv,
-          dq, dv, softmax_scale, op_, lp, _stream_ptr(stream, dev))
+        out = _empty((q.shape[0], q.shape[1], v.shape[2]), torch.bfloat16, q, stream)
+    dev = torch.cuda.current_device()
+    code = _calls().prompt(dev, _stream_ptr(stream, dev), q, k, v, cu_seqlens, out, lse, softmax_scale)
+    if code != VPP_OK:
+        raise VppError("vpp_prompt_attn", code)
     return out
 
 

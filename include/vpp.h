@@ -559,24 +559,6 @@ int vpp_prompt_attn(const void *q, int64_t q_stride, const void *k,
                     float softmax_scale, void *out, float *lse, void *stream);
 
 /*
- * One of the calls above with its arguments, in their order, as an array of
- * 64-bit words: pointers and whole numbers as they are, a float as its 32-bit
- * pattern in the low half.  For bindings that convert arguments one by one,
- * which for thirty of them takes longer than the smallest of these kernels.
- * nargs other than the call's count, or a word that does not fit its argument,
- * returns VPP_ERR_INVALID.
- */
-typedef enum {
-    VPP_CALL_ROPE_APPEND = 1,
-    VPP_CALL_ROPE_APPEND_FP8 = 2,
-    VPP_CALL_DECODE_ATTN = 3,
-    VPP_CALL_DECODE_ATTN_FP8 = 4,
-    VPP_CALL_PROMPT_ATTN = 5
-} vpp_call_op;
-
-int vpp_call(int op, const void *args, int nargs);
-
-/*
  * Device status word: synchronises `stream`, stores the first error any
  * kernel of this library recorded since the last reset (VPP_OK if none) in
  * *code, and resets the word to VPP_OK.  Returns VPP_ERR_CUDA if the

@@ -2,7 +2,6 @@
 the host before any launch, so these run without a GPU."""
 
 import ctypes
-import struct
 
 import pytest
 
@@ -99,51 +98,6 @@ def test_empty_calls_are_no_ops(lib):
     assert lib.vpp_prompt_attn(*args(PRO, dict(T=0, q=None, k=None, v=None, cu=None, out=None, lse=None))) == vpp.VPP_OK
 
 
-def words(values):
-    return b"".join(struct.pack("=f4x", v) if isinstance(v, float) else struct.pack("=q", v or 0) for v in values)
-
-
-CALLS = [(1, ROPE, {}, "vpp_rope_append"), (3, DEC, {}, "vpp_decode_attn"), (5, PRO, {}, "vpp_prompt_attn")]
-
-
-@pytest.mark.parametrize("op,base,_,name", CALLS)
-def test_packed_call_checks_like_the_call(lib, op, base, _, name):
-    """Every argument, spoilt in turn, gives the same answer both ways (without a device, the answer of the good call is
-    the missing device's)."""
-    for key in [None] + list(base):
-        if key == "st":
-            continue
-        for spoilt in (None, 3, -1, BAD):
-            if key is not None and isinstance(base[key], float):
-                continue
-            a = args(base, {} if key is None else {key: spoilt})
-            narrow = key not in (None, "q", "k", "v", "qo", "ko", "kc", "vc", "bt", "cu", "ctx", "out", "lse", "ws", "cs")
-            if spoilt is None and narrow or (spoilt == -1 and not narrow) or (key == "wb"):
-                continue
-            if key is None:
-                a = args(base, dict(Hkv=3))  # refused, so that nothing is launched where there is a device
-            elif spoilt == 3 and key in ("rows", "mb", "nb", "batch", "T", "il"):
-                continue  # a good value: would launch
-            elif key in ("ko", "ctx") and spoilt is None or (key == "lse" and spoilt is None):
-                continue  # may be missing: would launch
-            elif spoilt == BAD and (key == "lse" or key == "ctx" or key == "cu" or key == "bt" or key == "cs" or narrow):
-                continue
-            want = getattr(lib, name)(*a)
-            assert want != vpp.VPP_OK
-            assert lib.vpp_call(op, words(a), len(a)) == want, (key, spoilt)
-
-
-def test_packed_call_refuses_other_counts_and_wide_words(lib):
-    for op, base, _, _name in CALLS:
-        a = args(base, {})
-        assert lib.vpp_call(op, words(a) + bytes(8), len(a) + 1) == INV
-        assert lib.vpp_call(op, words(a), len(a) - 1) == INV
-        assert lib.vpp_call(op, words(args(base, dict(H=8 + (1 << 32)))), len(a)) == INV
-    assert lib.vpp_call(0, words([0] * 40), 29) == INV
-    assert lib.vpp_call(9, words([0] * 40), 29) == INV
-    assert lib.vpp_call(1, None, 29) == INV
-
-
 def test_workspace_sizes(lib):
     assert vpp.decode_attn_workspace_size(0, 8, 2, 128, 128) == 0
     assert vpp.decode_attn_workspace_size(4, 7, 2, 128, 128) == 0
@@ -159,3 +113,89 @@ def test_binding_refuses_host_tensors():
         x = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
         vpp.vpp_prompt_attn(x, x, x, torch.zeros(2, dtype=torch.int32))
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+class Fake:
+    """What the call module reads of a tensor."""
+
+    def __init__(self, *shape, dtype=None, device=0, ptr=P, stride=None):
+        import torch
+        self.shape, self.dtype, self._device, self._ptr = tuple(shape), dtype or torch.bfloat16, device, ptr
+        dense, n = [], 1
+        for s in reversed(shape):
+            dense.insert(0, n)
+            n *= s
+        self._stride = tuple(stride or dense)
+        self._dense = self._stride == tuple(dense)
+
+    def get_device(self):
+        return self._device
+
+    def data_ptr(self):
+        return self._ptr
+
+    def is_contiguous(self):
+        return self._dense
+
+    def stride(self):
+        return self._stride
+
+
+def test_the_call_module_checks_tensors(lib):
+    """Types, devices, shapes and strides, on stand-ins for tensors; what passes reaches the library, whose own refusal
+    (head dims of 96) comes back as its status."""
+    torch = pytest.importorskip("torch")
+    c = vpp._calls()
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+
+    def prompt(**kw):
+        a = dict(q=Fake(5, 8, 96), k=Fake(5, 4, 96), v=Fake(5, 4, 64), cu=Fake(3, dtype=i32), out=Fake(5, 8, 64), lse=Fake(8, 5, dtype=f32))
+        return c.prompt(0, 0, *{**a, **kw}.values(), 0.0)
+
+    assert prompt() == UNS and prompt(lse=None) == UNS
+    assert prompt(q=Fake(5, 8, 96, stride=(2000, 96, 1))) == UNS  # part of a wider projection
+    bad = [dict(q=Fake(5, 8, 96, dtype=f32)), dict(q=Fake(5, 8, 96, device=1)), dict(q=Fake(5, 8, 96, device=-1)), dict(q=Fake(5, 768)),
+           dict(q=Fake(5, 8, 96, stride=(768, 1, 8))), dict(q=Fake(5, 8, 96, stride=(800, 100, 1))), dict(k=Fake(4, 4, 96)), dict(k=Fake(5, 4, 64)),
+           dict(k=Fake(5, 2, 96)), dict(v=Fake(6, 4, 64)), dict(cu=Fake(3, dtype=torch.int64)), dict(cu=Fake(3, dtype=i32, stride=(2,))),
+           dict(cu=Fake(3, 1, dtype=i32)), dict(out=Fake(5, 8, 96)), dict(out=Fake(5, 8, 64, stride=(1024, 64, 1))), dict(lse=Fake(5, 8, dtype=f32)),
+           dict(lse=Fake(8, 5))]
+    for b in bad:
+        with pytest.raises(ValueError):
+            prompt(**b)
+
+    def decode(**kw):
+        a = dict(q=Fake(3, 8, 96), kc=Fake(6, 64, 4, 96), vc=Fake(6, 64, 4, 64), ks=None, vs=None, table=Fake(3, 4, dtype=i32),
+                 ctx=Fake(3, dtype=i32), out=Fake(3, 8, 64), lse=Fake(8, 3, dtype=f32))
+        return c.decode(0, 0, *{**a, **kw}.values(), 0.0, 0, 0)
+
+    fp8 = dict(kc=Fake(6, 64, 4, 96, dtype=u8), vc=Fake(6, 64, 4, 64, dtype=u8), ks=Fake(4, dtype=f32), vs=Fake(4, dtype=f32))
+    assert decode() == UNS and decode(**fp8) == UNS
+    bad = [dict(q=Fake(3, 8, 64)), dict(kc=Fake(6, 32, 4, 96)), dict(vc=Fake(5, 64, 4, 64)), dict(vc=Fake(6, 64, 2, 64)), dict(kc=fp8["kc"]),
+           dict(table=Fake(2, 4, dtype=i32)), dict(table=Fake(3, 4)), dict(table=Fake(12, dtype=i32)), dict(ctx=Fake(2, dtype=i32)), dict(out=Fake(3, 8, 96)),
+           dict(lse=Fake(3, 8, dtype=f32)), {**fp8, "ks": Fake(3, dtype=f32)}, {**fp8, "vs": Fake(4)}, {**fp8, "kc": Fake(6, 64, 4, 96)},
+           dict(kc=Fake(6, 64, 4, 96, device=2))]
+    for b in bad:
+        with pytest.raises(ValueError):
+            decode(**b)
+    assert decode(q=Fake(3, 8, 96, stride=(1000, 96, 1))) == UNS
+    with pytest.raises(ValueError):
+        decode(table=Fake(3, 1 << 33, dtype=i32))
+
+    def rope(**kw):
+        a = dict(q=Fake(5, 8, 96), k=Fake(5, 4, 96), v=Fake(5, 4, 64), cs=Fake(32, 64, dtype=f32), kc=Fake(6, 64, 4, 96), vc=Fake(6, 64, 4, 64), ks=None,
+                 vs=None, table=Fake(2, 4, dtype=i32), cu=Fake(3, dtype=i32), ctx=Fake(2, dtype=i32), qo=Fake(5, 8, 96), ko=None, start=0, il=False)
+        return c.rope(0, 0, *{**a, **kw}.values())
+
+    assert rope() == UNS and rope(ctx=None) == UNS and rope(**fp8) == UNS and rope(q=None, qo=None) == UNS
+    assert rope(kc=None, vc=None, v=None, table=None, ko=Fake(5, 4, 96)) == UNS
+    bad = [dict(q=Fake(4, 8, 96)), dict(qo=Fake(5, 4, 96)), dict(q=None), dict(k=Fake(5, 2, 96)), dict(v=Fake(5, 4, 96)), dict(cs=Fake(32, 64)), dict(cs=Fake(64, dtype=f32)),
+           dict(table=Fake(3, 4, dtype=i32)), dict(ctx=Fake(3, dtype=i32)), dict(ko=Fake(5, 8, 96)), dict(kc=Fake(6, 64, 4, 64)),
+           {**fp8, "ks": Fake(3, dtype=f32)}]
+    for b in bad:
+        with pytest.raises(ValueError):
+            rope(**b)
+    for f, n in ((c.rope, 17), (c.decode, 14), (c.prompt, 9)):
+        with pytest.raises(TypeError):
+            f(*[0] * (n - 1))
+    with pytest.raises((AttributeError, TypeError)):
+        c.prompt(0, 0, 1, 2, 3, 4, 5, 6, 0.0)
