@@ -17,6 +17,25 @@ struct VarlenPlan {
   int32_t ctx[kMaxBatch];           // total keys of each sequence (incl. new tokens)
 };
 
+// Launches a kernel that may be placed before the one before it in the stream has
+// ended (programmatic dependent launch); the kernel calls grid_wait() before its
+// first global access.
+template <typename... A>
+cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                              const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Kernel launchers (defined in the .cu files, called from api.cu).
 cudaError_t launch_kv_append(const void* k_new, const void* v_new, bool in_fp32, void* k_cache,
                              void* v_cache, const int32_t* block_table, int32_t num_blocks,

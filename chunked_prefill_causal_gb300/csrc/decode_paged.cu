@@ -209,8 +209,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
   const int h = blockIdx.x - col * p.kv_heads;
   const int G = p.heads / p.kv_heads;
 
-  // The join kernel may be placed beside this one; it waits for its end.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_next();  // the join kernel may be placed beside this one
 
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
@@ -220,6 +219,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
     }
     fence_mbar_init();
   }
+  grid_wait();
   // ---- this column's pages: warp w adds up the w-th fifth of the sequences,
   // and the one whose range holds the column's first page finds it.
   const int per = (p.batch + 4) / 5;
@@ -705,7 +705,8 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
   constexpr int PER = DV / 32;
   __shared__ float so[4][DV];
   __shared__ float2 sml[4];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_launch_next();
+  grid_wait();
   const int c = blockIdx.x, hq = blockIdx.y;
   const JoinDesc d = ws.desc[c];
   if (d.b < 0) return;
@@ -783,20 +784,10 @@ cudaError_t launch_t(const PagedDecodeParams& p, const CUtensorMap* maps, const 
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  paged_decode_kernel<DQ, DV, F8, NG><<<cols * p.kv_heads, kThreads, C::SMEM, stream>>>(maps[0], maps[1], maps[2], maps[3],
-                                                                                  p, ws, cols);
-  e = cudaGetLastError();
+  e = launch_overlapped(paged_decode_kernel<DQ, DV, F8, NG>, dim3(cols * p.kv_heads), kThreads, C::SMEM, stream, maps[0],
+                        maps[1], maps[2], maps[3], p, ws, cols);
   if (e != cudaSuccess || cols == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(cols, p.heads);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<DV>, p, ws);
+  return launch_overlapped(decode_join_kernel<DV>, dim3(cols, p.heads), 128, 0, stream, p, ws);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }

@@ -285,6 +285,8 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
     tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
     tmem_relinquish();
   }
+  grid_launch_next();
+  grid_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -816,8 +818,8 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
   const int64_t tokens = S::TILES * (kTileM / (p.heads / p.kv_heads));
   const int64_t items = (p.total / tokens + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
   if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
-  prompt_attn_kernel<DQ, DV, PAIR><<<static_cast<int>(items), S::THREADS, S::SMEM, stream>>>(tm_q, tm_k, tm_v, p);
-  return cudaGetLastError();
+  return launch_overlapped(prompt_attn_kernel<DQ, DV, PAIR>, dim3(static_cast<unsigned>(items)), S::THREADS, S::SMEM, stream,
+                           tm_q, tm_k, tm_v, p);
 }
 
 // One query tile a CTA, two CTAs per SM, where the second tile of a pair would

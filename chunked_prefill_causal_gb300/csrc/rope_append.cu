@@ -129,6 +129,8 @@ __device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (
 template <bool IL, bool F8>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(const __grid_constant__ RopeParams p,
                                                                               const int tile) {
+  grid_launch_next();
+  grid_wait();
   // Thread i of the token's `wide` threads.
   const int wide = kRopeThreads / tile;
   const int i = threadIdx.x % wide;
@@ -262,13 +264,9 @@ cudaError_t launch_rope_append(const RopeParams& p, bool interleaved, bool fp8, 
   const int passes = ((p.q ? p.heads : 0) + p.kv_heads + pass - 1) / pass;
   const int64_t want = (static_cast<int64_t>(kRopeWaves) * kRopeCtas * num_sms + ctas - 1) / ctas;
   const dim3 grid(static_cast<unsigned>(ctas), static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(passes, want))));
-  if (interleaved)
-    fp8 ? rope_append_kernel<true, true><<<grid, kRopeThreads, 0, stream>>>(p, tile)
-        : rope_append_kernel<true, false><<<grid, kRopeThreads, 0, stream>>>(p, tile);
-  else
-    fp8 ? rope_append_kernel<false, true><<<grid, kRopeThreads, 0, stream>>>(p, tile)
-        : rope_append_kernel<false, false><<<grid, kRopeThreads, 0, stream>>>(p, tile);
-  return cudaGetLastError();
+  const auto kernel = interleaved ? (fp8 ? rope_append_kernel<true, true> : rope_append_kernel<true, false>)
+                                  : (fp8 ? rope_append_kernel<false, true> : rope_append_kernel<false, false>);
+  return launch_overlapped(kernel, grid, kRopeThreads, 0, stream, p, tile);
 }
 
 }  // namespace vpp
