@@ -18,17 +18,17 @@
 // read each key from HBM once per tile of queries: 32768 tokens in prompts of
 // 512 moved 1.25 GB for the 0.4 GB that there are.)
 //
-// Persistent CTAs.  A resident CTA takes over the grid's next one that has not
+// Persistent CTAs.  A resident CTA takes over another one of the grid that has not
 // started (cluster launch control), so the items go to whichever SM is free, in
-// order, without a counter in memory.  The chunk kernel's one-item CTAs cost
+// about their order, without a counter in memory.  The chunk kernel's one-item CTAs cost
 // about 8 us each besides their keys (launch, TMEM, first loads, drain, output),
 // most of the time of short prompts; here the next item's Q and K/V copies and its
 // first Q K^T run while the last softmax and the output of the current one do.
 //
 //   warp 0      TMA producer (Q of the item, then K and V tiles, ring of 16 KB slots)
 //   warp 1, 3   MMA issuers of query tiles A and B, taking turns
-//   warp 2      TMEM; finds the items ahead of their use and hands them out
-//               through four shared-memory entries; zeroes the V rows of other
+//   warp 2      TMEM; finds the next item while one is under way and hands it out
+//               through shared memory; zeroes the V rows of other
 //               sequences in an item's last tile (P = 0 times whatever they hold
 //               must stay 0; their K rows are masked before the softmax)
 //   warps 4-7, 8-11   softmax and output of tiles A and B
@@ -48,7 +48,7 @@ namespace {
 
 using namespace attn_detail;
 
-constexpr int kEntries = 4;  // items handed out ahead
+constexpr int kEntries = 4;  // items handed out at most (two ahead)
 
 struct Item {
   int start, len;  // the sequence's rows
@@ -91,93 +91,98 @@ struct PShape {
   __device__ __forceinline__ static int tile_slots(int t) { return S::tile_slots(t); }
 };
 
-// The work list, by one warp.  The first kHeld x 32 sequences' item counts stay
-// in registers (a sequence per lane and register), those of further ones are
-// read again in each pass.  Items are asked for in increasing order, so a scan
-// goes on where the one before left it.
+// The work list, by one warp.  Sequences of more than half the items of the
+// longest one left form a class; within it they come in their order.  A lane
+// holds one of 32 sequences; items mostly come in increasing order, so most are
+// found among the 32 at hand, and an earlier one starts the scan over.
 struct Finder {
-  static constexpr int kHeld = 8;
   const PromptParams& p;
-  int tokens, lane;     // tokens of an item
-  int np[kHeld];
-  int lo, hi;           // the class: sequences with lo <= np < hi
-  int before, items;    // items of the classes before, and of this one
-  int scan_base, scan;  // sequences scanned in this class, and their items
-  int np_b;             // np of the sequence found
-  int pair;             // index of the item in it
-  __device__ __forceinline__ Finder(const PromptParams& p_, int tokens_) : p(p_), tokens(tokens_) {
-    lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) np[k] = pairs(32 * k + lane);
-    lo = hi = INT_MAX;
-    before = items = scan_base = scan = 0;
-  }
-  __device__ __forceinline__ int pairs(int b) const {
+  int tokens, lane;    // tokens of an item
+  int lo, hi;          // the class: sequences of lo <= items < hi
+  int before, items;   // items of the classes before, and of this one
+  int base, scan;      // first sequence at hand, and the class's items before it
+  int start, len;      // this lane's sequence
+  int n, inc;          // its items (0 outside the class), and with those of the lanes before
+  int total;           // items of all sequences, once known
+  __device__ __forceinline__ Finder(const PromptParams& p_, int tokens_)
+      : p(p_), tokens(tokens_), lane(threadIdx.x & 31), lo(INT_MAX), hi(INT_MAX), before(0), items(0), base(0), scan(0),
+        total(INT_MAX) {}
+  // Items of sequence b; its rows in start and len.
+  __device__ __forceinline__ int read(int b, int* first, int* length) const {
+    const int at = min(b, p.batch - 1);
+    const int s = __ldg(p.cu + at), e = __ldg(p.cu + at + 1);
+    *first = s;
+    *length = e - s;
     if (b >= p.batch) return 0;
-    const int start = __ldg(p.cu + b), end = __ldg(p.cu + b + 1);
-    if (start < 0 || end < start || end > p.total) {
+    if (s < 0 || e < s || e > p.total) {
       if (blockIdx.x == 0) record_status(p.status, kStatusInvalid);
       return 0;
     }
-    return (end - start + tokens - 1) / tokens;
+    return (e - s + tokens - 1) / tokens;
   }
-  // np of sequence base + lane (base a multiple of 32).
-  __device__ __forceinline__ int held(int base) const {
-    int n = 0;
+  __device__ __forceinline__ void load() {
+    n = read(base + lane, &start, &len);
+    if (n < lo || n >= hi) n = 0;
+    inc = n;
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (base == 32 * k) n = np[k];
-    return base >= 32 * kHeld ? pairs(base + lane) : n;
-  }
-  // The sequence of item i, or -1 past the last one.
-  __device__ __forceinline__ int find(int i) {
-    while (i >= before + items) {
-      // the next class: the longest sequences left, down to 3/4 of their length
-      before += items;
-      hi = lo;
-      int top = 0;
-#pragma unroll 4
-      for (int base = 0; base < p.batch; base += 32) {
-        const int n = held(base);
-        if (n < hi) top = max(top, n);
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (top == 0) {
-        items = 0;
-        lo = 0;
-        return -1;
-      }
-      lo = top - top / 4;
-      int sum = 0;
-#pragma unroll 4
-      for (int base = 0; base < p.batch; base += 32) {
-        const int n = held(base);
-        if (n >= lo && n < hi) sum += n;
-      }
-      items = __reduce_add_sync(0xffffffffu, sum);
-      scan_base = scan = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    const int want = i - before;  // among the class's items
-    for (; scan_base < p.batch; scan_base += 32) {
-      int n = held(scan_base);
-      if (n < lo || n >= hi) n = 0;
-      int inc = n;  // inclusive prefix over the lanes
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+  }
+  // Goes on to the next class; false behind the last one.
+  __device__ __forceinline__ bool next_class() {
+    before += items;
+    hi = lo;
+    int top = 0, sum = 0, x, y;
+#pragma unroll 1
+    for (int b = lane; b < p.batch + 31 - (p.batch + 31) % 32 + lane; b += 32) {
+      const int m = read(b, &x, &y);
+      if (m < hi) top = max(top, m);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    lo = top / 2 + 1;
+#pragma unroll 1
+    for (int b = lane; b < p.batch + 31 - (p.batch + 31) % 32 + lane; b += 32) {
+      const int m = read(b, &x, &y);
+      if (m >= lo && m < hi) sum += m;
+    }
+    items = __reduce_add_sync(0xffffffffu, sum);
+    base = scan = 0;
+    load();
+    return top > 0;
+  }
+  // Item i: its sequence's rows and its index in the sequence (the last tokens
+  // come first); false when there is no such item.
+  __device__ __forceinline__ bool find(int i, int* first, int* length, int* index) {
+    if (i >= total) return false;
+    if (i < before) {
+      lo = hi = INT_MAX;
+      before = items = 0;
+    } else if (i < before + scan) {
+      base = scan = 0;
+      load();
+    }
+    while (i >= before + items)
+      if (!next_class()) {
+        total = before;
+        return false;
       }
+    const int want = i - before;
+    while (true) {
       const uint32_t hit = __ballot_sync(0xffffffffu, want < scan + inc);
       if (hit) {
         const int l = __ffs(hit) - 1;
-        np_b = __shfl_sync(0xffffffffu, n, l);
-        // longest first within the sequence
-        pair = np_b - 1 - (want - (scan + __shfl_sync(0xffffffffu, inc, l) - np_b));
-        return scan_base + l;
+        *first = __shfl_sync(0xffffffffu, start, l);
+        *length = __shfl_sync(0xffffffffu, len, l);
+        *index = scan + __shfl_sync(0xffffffffu, inc, l) - 1 - want;
+        return true;
       }
       scan += __shfl_sync(0xffffffffu, inc, 31);
+      base += 32;
+      if (base >= p.batch) return false;  // (only when the ranges overlap so that the counts overflow)
+      load();
     }
-    return -1;  // (only when the ranges overlap so that the counts overflow)
   }
 };
 
@@ -373,62 +378,65 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
     } else if (warp == 2) {
       // --------------------------------------- items, and V rows of other sequences
       Finder finder(p, S::TILES * T);
-      int published = 0, requests = 0;
+      int requests = 0;
       bool ok = true;
-      int idx = blockIdx.x;  // CTA whose item is handed out next, -1: none left
-      auto next_idx = [&]() {
-        __syncwarp();
-        if (lane == 0) {
-          fence_proxy_async_smem();  // after the reads of the answer before
-          mbar_arrive_expect_tx(bar(S::B_CLC), 16);
-          clc_request(smem_u32(clc), bar(S::B_CLC));
-        }
-        ok = warp_wait(bar(S::B_CLC), requests & 1, p.status, abort_flag);
-        if (!ok) mbar_wait_for(bar(S::B_CLC), requests & 1, kCleanupNs);  // lands before the CTA exits
-        ++requests;
-        idx = ok ? clc_answer(smem_u32(clc)) : -1;
-      };
-      auto publish = [&]() {
-        Item it{0, 0, 0, 0, 0, 0, {0, 0}};
+      Item it;
+      // Item of CTA `idx`; false if it has none (the grid's size is an upper bound).
+      auto item_of = [&](int idx) {
         const int item = idx / p.kv_heads;
-        const int b = idx < 0 ? -1 : finder.find(item);
-        if (b >= 0) {
-          it.start = __ldg(p.cu + b);
-          it.len = __ldg(p.cu + b + 1) - it.start;
-          it.tok0 = finder.pair * S::TILES * T;
-          it.g = idx - item * p.kv_heads;
-          it.na = (min(it.tok0 + T, it.len) + kTileN - 1) / kTileN;
-          it.nb = PAIR && it.tok0 + T < it.len ? (min(it.tok0 + 2 * T, it.len) + kTileN - 1) / kTileN : 0;
+        int index;
+        if (!finder.find(item, &it.start, &it.len, &index)) return false;
+        it.tok0 = index * S::TILES * T;
+        it.g = idx - item * p.kv_heads;
+        it.na = (min(it.tok0 + T, it.len) + kTileN - 1) / kTileN;
+        it.nb = PAIR && it.tok0 + T < it.len ? (min(it.tok0 + 2 * T, it.len) + kTileN - 1) / kTileN : 0;
+        return true;
+      };
+      // The next item: of a CTA of the grid that has not started, until one has an
+      // item or none is left.  (The order in which they are given is the
+      // hardware's; it is nearly, not always, that of their indexes.)
+      auto next_item = [&]() {
+        while (ok) {
+          __syncwarp();
+          if (lane == 0) {
+            fence_proxy_async_smem();  // after the reads of the answer before
+            mbar_arrive_expect_tx(bar(S::B_CLC), 16);
+            clc_request(smem_u32(clc), bar(S::B_CLC));
+          }
+          ok = warp_wait(bar(S::B_CLC), requests & 1, p.status, abort_flag);
+          if (!ok) mbar_wait_for(bar(S::B_CLC), requests & 1, kCleanupNs);  // lands before the CTA exits
+          ++requests;
+          const int idx = ok ? clc_answer(smem_u32(clc)) : -1;
+          if (idx < 0) break;
+          if (item_of(idx)) return;
         }
-        const int e = published % kEntries;
-        if (published >= kEntries &&
-            !(ok = warp_wait(bar(S::B_IE + e), (published / kEntries - 1) & 1, p.status, abort_flag)))
-          return;
+        it.len = 0;
+      };
+      int published = 0;
+      auto publish = [&]() {
         if (lane == 0) {
-          entries[e] = it;
-          mbar_arrive(bar(S::B_IF + e));
+          entries[published % kEntries] = it;
+          mbar_arrive(bar(S::B_IF + published % kEntries));
         }
         __syncwarp();
         ++published;
       };
+      if (!item_of(blockIdx.x)) next_item();
       publish();
       int base = 0;
       uint32_t tmp_phase = 0u;
       for (int i = 0; ok; ++i) {
-        const Item it = entries[i % kEntries];  // (overwritten by item i + 4 at the earliest)
-        if (it.len == 0) break;
-        // item i + 1
-        next_idx();
-        if (ok) publish();
-        if (!ok) break;
-        const int n = max(it.na, it.nb);
-        const int t = 2 * (base + n) - 1;
-        const int r0 = it.len - (n - 1) * kTileN;
-        if (r0 < kTileN) {
-          const int tb = t % S::NB;
-          if (!(ok = warp_wait(bar(S::B_TMP + tb), (tmp_phase >> tb) & 1u, p.status, abort_flag))) break;
+        const Item cur = entries[i % kEntries];
+        if (cur.len == 0) break;
+        const int n = max(cur.na, cur.nb);
+        // V rows past the sequence in the item's last tile
+        auto zero_rows = [&]() {
+          const int t = 2 * (base + n) - 1, tb = t % S::NB, pos = S::tile_pos(t);
+          const int r0 = cur.len - (n - 1) * kTileN;
+          if (r0 >= kTileN) return;
+          ok = warp_wait(bar(S::B_TMP + tb), (tmp_phase >> tb) & 1u, p.status, abort_flag);
+          if (!ok) return;
           tmp_phase ^= 1u << tb;
-          const int pos = S::tile_pos(t);
           for (int u = r0 * 8 + lane; u < kTileN * 8; u += 32)  // 16-byte units of rows r0 .. 127
 #pragma unroll
             for (int c = 0; c < S::NVC; ++c)
@@ -437,12 +445,24 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(S::B_FULL + tb));
+        };
+        // Further items are asked for once every role has begun this one, the
+        // next one, or two when this is short (an answer, its sequence and its
+        // first copies take as long as a short item: 1024 prompts of 32 tokens took
+        // 194 us with one ahead, 157 us with two).  Asked for as early as the
+        // entries allow, a CTA holds items that others could have run: three prompts
+        // with 128 heads took 182 us, their CTAs ending 113 to 185 us in, now 152 us.
+        // A short item's own rows come first.
+        const bool is_short = n <= 2;
+        if (is_short) zero_rows();
+        if (ok) ok = warp_wait(bar(S::B_IE + i % kEntries), (i / kEntries) & 1, p.status, abort_flag);
+        while (ok && it.len > 0 && published <= i + (is_short ? 2 : 1)) {
+          next_item();
+          if (ok) publish();
         }
+        if (ok && !is_short) zero_rows();
         base += n;
       }
-      // Past the last item the grid has only empty ones (its size is an upper
-      // bound): they are taken here until none is left.
-      while (ok && idx >= 0) next_idx();
     } else if ((warp == 1 || (PAIR && warp == 3)) && lane == 0) {
       // ---------------------------------------------------- MMA issuer
       const int x = warp == 1 ? 0 : 1;
