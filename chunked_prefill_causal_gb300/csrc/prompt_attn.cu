@@ -16,7 +16,11 @@
 // head by head: the heaviest start first, and the items that read the same keys
 // and values run at the same time.  (Ordered by their weight alone, equal prompts
 // read each key from HBM once per tile of queries: 32768 tokens in prompts of
-// 512 moved 1.25 GB for the 0.4 GB that there are.)
+// 512 moved 1.25 GB for the 0.4 GB that there are.)  Where the keys and values of a
+// sequence's heads together outgrow L2, all its items of 32 heads come before the next
+// 32 heads': two prompts of 4096 tokens, 128 heads of their own keys, 192 dims, take
+// 1102 us, all heads together 1185.  Within L2 it loses: eight of 1024 tokens 399 and
+// 390 us.
 //
 // Persistent CTAs.  A resident CTA takes over another one of the grid that has not
 // started (cluster launch control), so the items go to whichever SM is free, in
@@ -36,7 +40,17 @@
 // The two tiles of a pair may need different numbers of key tiles (nA <= nB; B is
 // absent when the sequence ends in A), and each runs its own number.
 //
-// Bound by the tensor core for long prompts, by the chain of one item for short ones.
+// Rounding: a row's P is rounded to bf16 as the P V operand (relative 2^-8, against V
+// in bf16); its sum, the denominator, keeps the float32 values, as O and the scores do.
+//
+// Bound by the tensor core and the softmax that feeds it for long prompts: one of
+// 16384 tokens, 32/8 heads of 128, takes 1350 to 1380 us on a GB300, 1593 to 1629 TFLOP/s (83 to 85% of the
+// cuBLAS rate; tensor pipe active 67% of the cycles, issue slots 41%).  Bound by the
+// chain of one item (first loads, first softmax, drain, output: 2.5 us beside its keys)
+// for short ones: 24 prompts of 5 to 2500 tokens take 111 us (941 TFLOP/s, tensor pipe
+// 46%).  At 192 dims the ring holds a K tile, its V tile and the next K tile, no
+// more, and each item starts by loading 96 KB of Q: three prompts of 300 to 1900
+// tokens, 128 heads of their own keys, take 151 us, 2.3 times their bytes' time.
 #include <algorithm>
 #include <climits>
 
@@ -49,6 +63,10 @@ namespace {
 using namespace attn_detail;
 
 constexpr int kEntries = 4;  // items handed out at most (two ahead)
+
+// Kv heads of a sequence that go together where not all of them fit into L2.
+constexpr int kHeadGroup = 32;
+constexpr int64_t kKeptBytes = 100ll << 20;  // of the 129 MB
 
 struct Item {
   int start, len;  // the sequence's rows
@@ -115,7 +133,8 @@ struct Finder {
     *length = e - s;
     if (b >= p.batch) return 0;
     if (s < 0 || e < s || e > p.total) {
-      if (blockIdx.x == 0) record_status(p.status, kStatusInvalid);
+      // (by every CTA: which ones start, and which are taken over, is the hardware's choice)
+      record_status(p.status, kStatusInvalid);
       return 0;
     }
     return (e - s + tokens - 1) / tokens;
@@ -386,8 +405,18 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
         const int item = idx / p.kv_heads;
         int index;
         if (!finder.find(item, &it.start, &it.len, &index)) return false;
-        it.tok0 = index * S::TILES * T;
         it.g = idx - item * p.kv_heads;
+        if (p.kv_heads > kHeadGroup && static_cast<int64_t>(it.len) * p.kv_heads * (DQ + DV) * 2 > kKeptBytes) {
+          // groups of heads, the sequence's items of one group before the next one's
+          const int n = (it.len + S::TILES * T - 1) / (S::TILES * T);
+          const int at = (n - 1 - index) * p.kv_heads + it.g;  // in the sequence's order
+          const int first = at / (n * kHeadGroup) * kHeadGroup;
+          const int heads = min(kHeadGroup, p.kv_heads - first);
+          const int rest = at - first * n;
+          index = n - 1 - rest / heads;
+          it.g = first + rest % heads;
+        }
+        it.tok0 = index * S::TILES * T;
         it.na = (min(it.tok0 + T, it.len) + kTileN - 1) / kTileN;
         it.nb = PAIR && it.tok0 + T < it.len ? (min(it.tok0 + 2 * T, it.len) + kTileN - 1) / kTileN : 0;
         return true;

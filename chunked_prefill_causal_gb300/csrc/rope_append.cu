@@ -17,7 +17,7 @@
 // Bound by HBM for many tokens (each input is read and each output written
 // once), by the latency of the chain lengths -> block and table row -> stores
 // for few.  Measured on a GB300: 16384 tokens of 64 + 8 heads of 128, 679 MB,
-// in 104.5 us (6.5 TB/s, 96% of the copy bandwidth); 4 decode tokens in 3.1 us.
+// in 104.4 us (6.5 TB/s, 96% of the copy bandwidth); 4 decode tokens in 2.8 us.
 //
 // Work split.  A row (one head of one token) is d / 16 tasks of two 16-byte
 // vectors: eight pairs of the rotated dims (both ends of the pairs, so that one

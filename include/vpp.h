@@ -451,7 +451,8 @@ size_t vpp_topk_chunk_attn_workspace_size(int64_t chunk_len, int32_t topk,
  * are not allowed, and two sequences must not share the block of a new token.
  *
  * Rows from cu_seqlens_q[batch] to total_q - 1, and the rows of a sequence
- * with ctx_lens[b] == 0, are padding: nothing is read or written for them.
+ * with ctx_lens[b] == 0, are padding: what they hold is ignored and nothing
+ * is written for them.
  * Nothing is written, and VPP_ERR_INVALID is recorded, for a token whose
  * position is outside the table, whose block is outside the pool or the block
  * table's row, or whose ctx_lens[b] < q_len_b, and for rows past total_q.

@@ -218,3 +218,25 @@ def test_growing_scores_rescale():
     lse = torch.empty((H, n), device=DEV)
     out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse, softmax_scale=0.2)
     check_sequences(out, lse, q, k, v, cu, d, scale=0.2)
+
+
+@pytest.mark.parametrize("Hkv,lens", [(40, [300, 10500, 7]), (64, [6500, 2])])
+def test_heads_in_groups(Hkv, lens):
+    """Keys and values of all heads beyond 100 MB (the items then go by groups of heads, the last group a partial one):
+    sampled rows against the formula, and every row written once or more."""
+    d = 64
+    cu = starts(lens)
+    T = int(cu[-1])
+    q, k, v = randn((T, Hkv, d), 31), randn((T, Hkv, d), 32), randn((T, Hkv, d), 33)
+    out = torch.full((T, Hkv, d), float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((Hkv, T), float("nan"), device=DEV)
+    vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), out=out, lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    assert bool(torch.isfinite(out).all()) and bool(torch.isfinite(lse).all())
+    for b, n in enumerate(lens):
+        lo = int(cu[b])
+        for t in sorted({0, n // 3, n // 2 + 1, n - 1}):
+            ref = attend(q[lo + t:lo + t + 1], k[lo:lo + t + 1], v[lo:lo + t + 1], d ** -0.5, False)
+            # (besides P's rounding, t + 1 products added up in float32)
+            check_attention(out[lo + t:lo + t + 1], lse[:, lo + t:lo + t + 1], ref, d, HALF_BF16 + (t + 1) * 2.0 ** -23,
+                            f"sequence {b} token {t}")
