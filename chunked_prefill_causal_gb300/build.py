@@ -1,6 +1,6 @@
 """Builds libvpp.so (sm_103a) in-tree: one nvcc -c per .cu file, in parallel,
 then one shared-library link with the CUDA runtime linked statically; and the
-binding's call module (csrc/pycall.c)."""
+binding's call module (csrc/pycall.cpp)."""
 
 from __future__ import annotations
 
@@ -41,18 +41,29 @@ def _stale(obj, src, hdr_mtime):
             or os.path.getmtime(obj) < hdr_mtime)
 
 
-def _call_module(out):
-    """Compiles csrc/pycall.c, the argument marshalling of the serving-step calls (a CPython extension module, host code
-    only), and returns its path."""
-    src, so = os.path.join(CSRC, "pycall.c"), os.path.join(out, "_vppcall.so")
+def call_module_path():
+    """The call module's file, which names the torch whose headers it was compiled with."""
+    import torch
+
+    return os.path.join(OUT_DIR, f"_vppcall-{torch.__version__}.so")
+
+
+def _call_module():
+    """Compiles csrc/pycall.cpp, the argument marshalling of the serving-step calls (a CPython extension module that reads
+    torch tensors; host code only)."""
+    import torch
+
+    src, so = os.path.join(CSRC, "pycall.cpp"), call_module_path()
     if _stale(so, src, os.path.getmtime(os.path.join(INCLUDE, "vpp.h"))):
-        cmd = [os.environ.get("CC", "gcc"), "-O2", "-fPIC", "-shared", "-Wall", "-I" + INCLUDE,
-               "-I" + sysconfig.get_paths()["include"], src, "-o", so + ".tmp"]
+        home = os.path.dirname(torch.__file__)
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I" + INCLUDE,
+               "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"), src, "-o", so + ".tmp",
+               "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"compiling pycall.c failed:\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compiling pycall.cpp failed:\n{r.stdout}\n{r.stderr}")
         os.replace(so + ".tmp", so)
-    return so
 
 
 def build(verbose: bool = False, jobs: int | None = None, extra_flags=(), out_dir: str | None = None,
@@ -65,7 +76,6 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=(), out_di
     out = out_dir or OUT_DIR
     lib = os.path.join(out, lib_name)
     os.makedirs(out, exist_ok=True)
-    _call_module(out)
     nvcc = _nvcc()
     hdr_mtime = max((os.path.getmtime(h) for h in _headers()), default=0.0)
     srcs = _sources()
@@ -82,12 +92,14 @@ def build(verbose: bool = False, jobs: int | None = None, extra_flags=(), out_di
             raise RuntimeError(f"nvcc failed on {os.path.basename(s)}:\n{r.stdout}\n{r.stderr}")
         return s, r.stderr
 
-    if todo:
-        n = jobs or min(len(todo), os.cpu_count() or 4)
-        with concurrent.futures.ThreadPoolExecutor(max_workers=n) as ex:
-            for s, err in ex.map(compile_one, todo):
-                if verbose and err:
-                    sys.stderr.write(f"--- {os.path.basename(s)}\n{err}")
+    n = jobs or min(len(todo) + 1, os.cpu_count() or 4)
+    with concurrent.futures.ThreadPoolExecutor(max_workers=n) as ex:
+        call = ex.submit(_call_module) if out == OUT_DIR else None
+        for s, err in ex.map(compile_one, todo):
+            if verbose and err:
+                sys.stderr.write(f"--- {os.path.basename(s)}\n{err}")
+        if call:
+            call.result()
     if todo or not os.path.exists(lib) or any(os.path.getmtime(lib) < os.path.getmtime(o) for o in objs):
         tmp = lib + ".tmp"
         cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs, "-ldl", "-lpthread", "-lrt"]

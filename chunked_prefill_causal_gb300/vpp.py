@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libvpp.so (declared in include/vpp.h).
+"""Thin binding of libvpp.so (declared in include/vpp.h): ctypes, and for the
+serving-step calls a compiled module (csrc/pycall.cpp).
 
 Argument marshalling only: every function takes torch CUDA tensors, checks
 their dtype/shape/contiguity, passes raw pointers and the current stream to
@@ -15,6 +16,8 @@ import os
 import threading
 
 import torch
+
+from .build import call_module_path
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libvpp.so")
@@ -462,8 +465,7 @@ def vpp_topk_chunk_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_len, t
 
 # ----------------------------------------------------------------- lengths on the device
 # These calls are a few microseconds of GPU time at decode sizes: their arguments
-# are checked and passed on by a compiled module (csrc/pycall.c).
-CALL_PATH = os.path.join(_HERE, "_build", "_vppcall.so")
+# are checked and passed on by a compiled module (csrc/pycall.cpp).
 _call_module = None
 
 
@@ -471,14 +473,14 @@ def _calls():
     global _call_module
     if _call_module is None:
         lib = load()
-        if not os.path.exists(CALL_PATH):
-            raise RuntimeError(f"{CALL_PATH} not found: run __graft_entry__.build() first")
-        loader = importlib.machinery.ExtensionFileLoader("_vppcall", CALL_PATH)
+        path = call_module_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} not found: run __graft_entry__.build() first")
+        loader = importlib.machinery.ExtensionFileLoader("_vppcall", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_vppcall", loader))
         loader.exec_module(module)
         names = ("vpp_rope_append", "vpp_rope_append_fp8", "vpp_decode_attn", "vpp_decode_attn_fp8", "vpp_prompt_attn")
-        module.setup((torch.bfloat16, torch.float32, torch.int32, torch.uint8),
-                     tuple(ctypes.cast(getattr(lib, n), _c_void_p).value for n in names))
+        module.setup(tuple(ctypes.cast(getattr(lib, n), _c_void_p).value for n in names))
         _call_module = module
     return _call_module
 

@@ -115,87 +115,72 @@ def test_binding_refuses_host_tensors():
     assert ctypes.sizeof(ctypes.c_void_p) == 8
 
 
-class Fake:
-    """What the call module reads of a tensor."""
-
-    def __init__(self, *shape, dtype=None, device=0, ptr=P, stride=None):
-        import torch
-        self.shape, self.dtype, self._device, self._ptr = tuple(shape), dtype or torch.bfloat16, device, ptr
-        dense, n = [], 1
-        for s in reversed(shape):
-            dense.insert(0, n)
-            n *= s
-        self._stride = tuple(stride or dense)
-        self._dense = self._stride == tuple(dense)
-
-    def get_device(self):
-        return self._device
-
-    def data_ptr(self):
-        return self._ptr
-
-    def is_contiguous(self):
-        return self._dense
-
-    def stride(self):
-        return self._stride
+def fake(*shape, dtype=None, stride=None):
+    """A host tensor of this shape and stride; the call module takes them for device -1."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    return torch.zeros(shape, dtype=dtype) if stride is None else torch.empty_strided(shape, stride, dtype=dtype)
 
 
 def test_the_call_module_checks_tensors(lib):
-    """Types, devices, shapes and strides, on stand-ins for tensors; what passes reaches the library, whose own refusal
-    (head dims of 96) comes back as its status."""
+    """Types, devices, shapes and strides, on host tensors; what passes reaches the library, whose own refusal (head dims
+    of 96) comes back as its status before anything is read."""
     torch = pytest.importorskip("torch")
     c = vpp._calls()
     i32, f32, u8 = torch.int32, torch.float32, torch.uint8
 
-    def prompt(**kw):
-        a = dict(q=Fake(5, 8, 96), k=Fake(5, 4, 96), v=Fake(5, 4, 64), cu=Fake(3, dtype=i32), out=Fake(5, 8, 64), lse=Fake(8, 5, dtype=f32))
-        return c.prompt(0, 0, *{**a, **kw}.values(), 0.0)
+    def prompt(dev=-1, **kw):
+        a = dict(q=fake(5, 8, 96), k=fake(5, 4, 96), v=fake(5, 4, 64), cu=fake(3, dtype=i32), out=fake(5, 8, 64), lse=fake(8, 5, dtype=f32))
+        return c.prompt(dev, 0, *{**a, **kw}.values(), 0.0)
 
     assert prompt() == UNS and prompt(lse=None) == UNS
-    assert prompt(q=Fake(5, 8, 96, stride=(2000, 96, 1))) == UNS  # part of a wider projection
-    bad = [dict(q=Fake(5, 8, 96, dtype=f32)), dict(q=Fake(5, 8, 96, device=1)), dict(q=Fake(5, 8, 96, device=-1)), dict(q=Fake(5, 768)),
-           dict(q=Fake(5, 8, 96, stride=(768, 1, 8))), dict(q=Fake(5, 8, 96, stride=(800, 100, 1))), dict(k=Fake(4, 4, 96)), dict(k=Fake(5, 4, 64)),
-           dict(k=Fake(5, 2, 96)), dict(v=Fake(6, 4, 64)), dict(cu=Fake(3, dtype=torch.int64)), dict(cu=Fake(3, dtype=i32, stride=(2,))),
-           dict(cu=Fake(3, 1, dtype=i32)), dict(out=Fake(5, 8, 96)), dict(out=Fake(5, 8, 64, stride=(1024, 64, 1))), dict(lse=Fake(5, 8, dtype=f32)),
-           dict(lse=Fake(8, 5))]
+    assert prompt(q=fake(5, 8, 96, stride=(2000, 96, 1))) == UNS  # part of a wider projection
+    bad = [dict(q=fake(5, 8, 96, dtype=f32)), dict(dev=0), dict(dev=1), dict(q=fake(5, 768)),
+           dict(q=fake(5, 8, 96, stride=(768, 1, 8))), dict(q=fake(5, 8, 96, stride=(800, 100, 1))), dict(k=fake(4, 4, 96)), dict(k=fake(5, 4, 64)),
+           dict(k=fake(5, 2, 96)), dict(v=fake(6, 4, 64)), dict(cu=fake(3, dtype=torch.int64)), dict(cu=fake(3, dtype=i32, stride=(2,))),
+           dict(cu=fake(3, 1, dtype=i32)), dict(out=fake(5, 8, 96)), dict(out=fake(5, 8, 64, stride=(1024, 64, 1))), dict(lse=fake(5, 8, dtype=f32)),
+           dict(lse=fake(8, 5))]
     for b in bad:
         with pytest.raises(ValueError):
             prompt(**b)
 
-    def decode(**kw):
-        a = dict(q=Fake(3, 8, 96), kc=Fake(6, 64, 4, 96), vc=Fake(6, 64, 4, 64), ks=None, vs=None, table=Fake(3, 4, dtype=i32),
-                 ctx=Fake(3, dtype=i32), out=Fake(3, 8, 64), lse=Fake(8, 3, dtype=f32))
-        return c.decode(0, 0, *{**a, **kw}.values(), 0.0, 0, 0)
+    def decode(dev=-1, **kw):
+        a = dict(q=fake(3, 8, 96), kc=fake(6, 64, 4, 96), vc=fake(6, 64, 4, 64), ks=None, vs=None, table=fake(3, 4, dtype=i32),
+                 ctx=fake(3, dtype=i32), out=fake(3, 8, 64), lse=fake(8, 3, dtype=f32))
+        return c.decode(dev, 0, *{**a, **kw}.values(), 0.0, 0, 0)
 
-    fp8 = dict(kc=Fake(6, 64, 4, 96, dtype=u8), vc=Fake(6, 64, 4, 64, dtype=u8), ks=Fake(4, dtype=f32), vs=Fake(4, dtype=f32))
+    fp8 = dict(kc=fake(6, 64, 4, 96, dtype=u8), vc=fake(6, 64, 4, 64, dtype=u8), ks=fake(4, dtype=f32), vs=fake(4, dtype=f32))
     assert decode() == UNS and decode(**fp8) == UNS
-    bad = [dict(q=Fake(3, 8, 64)), dict(kc=Fake(6, 32, 4, 96)), dict(vc=Fake(5, 64, 4, 64)), dict(vc=Fake(6, 64, 2, 64)), dict(kc=fp8["kc"]),
-           dict(table=Fake(2, 4, dtype=i32)), dict(table=Fake(3, 4)), dict(table=Fake(12, dtype=i32)), dict(ctx=Fake(2, dtype=i32)), dict(out=Fake(3, 8, 96)),
-           dict(lse=Fake(3, 8, dtype=f32)), {**fp8, "ks": Fake(3, dtype=f32)}, {**fp8, "vs": Fake(4)}, {**fp8, "kc": Fake(6, 64, 4, 96)},
-           dict(kc=Fake(6, 64, 4, 96, device=2))]
+    bad = [dict(q=fake(3, 8, 64)), dict(kc=fake(6, 32, 4, 96)), dict(vc=fake(5, 64, 4, 64)), dict(vc=fake(6, 64, 2, 64)), dict(kc=fp8["kc"]),
+           dict(table=fake(2, 4, dtype=i32)), dict(table=fake(3, 4)), dict(table=fake(12, dtype=i32)), dict(ctx=fake(2, dtype=i32)), dict(out=fake(3, 8, 96)),
+           dict(lse=fake(3, 8, dtype=f32)), {**fp8, "ks": fake(3, dtype=f32)}, {**fp8, "vs": fake(4)}, {**fp8, "kc": fake(6, 64, 4, 96)}, dict(dev=0)]
     for b in bad:
         with pytest.raises(ValueError):
             decode(**b)
-    assert decode(q=Fake(3, 8, 96, stride=(1000, 96, 1))) == UNS
+    assert decode(q=fake(3, 8, 96, stride=(1000, 96, 1))) == UNS
     with pytest.raises(ValueError):
-        decode(table=Fake(3, 1 << 33, dtype=i32))
+        decode(table=torch.empty((3, 1 << 33), dtype=i32, device="meta"))
 
-    def rope(**kw):
-        a = dict(q=Fake(5, 8, 96), k=Fake(5, 4, 96), v=Fake(5, 4, 64), cs=Fake(32, 64, dtype=f32), kc=Fake(6, 64, 4, 96), vc=Fake(6, 64, 4, 64), ks=None,
-                 vs=None, table=Fake(2, 4, dtype=i32), cu=Fake(3, dtype=i32), ctx=Fake(2, dtype=i32), qo=Fake(5, 8, 96), ko=None, start=0, il=False)
-        return c.rope(0, 0, *{**a, **kw}.values())
+    def rope(dev=-1, **kw):
+        a = dict(q=fake(5, 8, 96), k=fake(5, 4, 96), v=fake(5, 4, 64), cs=fake(32, 64, dtype=f32), kc=fake(6, 64, 4, 96), vc=fake(6, 64, 4, 64), ks=None,
+                 vs=None, table=fake(2, 4, dtype=i32), cu=fake(3, dtype=i32), ctx=fake(2, dtype=i32), qo=fake(5, 8, 96), ko=None, start=0, il=False)
+        return c.rope(dev, 0, *{**a, **kw}.values())
 
     assert rope() == UNS and rope(ctx=None) == UNS and rope(**fp8) == UNS and rope(q=None, qo=None) == UNS
-    assert rope(kc=None, vc=None, v=None, table=None, ko=Fake(5, 4, 96)) == UNS
-    bad = [dict(q=Fake(4, 8, 96)), dict(qo=Fake(5, 4, 96)), dict(q=None), dict(k=Fake(5, 2, 96)), dict(v=Fake(5, 4, 96)), dict(cs=Fake(32, 64)), dict(cs=Fake(64, dtype=f32)),
-           dict(table=Fake(3, 4, dtype=i32)), dict(ctx=Fake(3, dtype=i32)), dict(ko=Fake(5, 8, 96)), dict(kc=Fake(6, 64, 4, 64)),
-           {**fp8, "ks": Fake(3, dtype=f32)}]
+    assert rope(kc=None, vc=None, v=None, table=None, ko=fake(5, 4, 96)) == UNS
+    bad = [dict(q=fake(4, 8, 96)), dict(qo=fake(5, 4, 96)), dict(q=None), dict(k=fake(5, 2, 96)), dict(v=fake(5, 4, 96)), dict(cs=fake(32, 64)), dict(cs=fake(64, dtype=f32)),
+           dict(table=fake(3, 4, dtype=i32)), dict(ctx=fake(3, dtype=i32)), dict(ko=fake(5, 8, 96)), dict(kc=fake(6, 64, 4, 64)),
+           {**fp8, "ks": fake(3, dtype=f32)}, dict(dev=0)]
     for b in bad:
         with pytest.raises(ValueError):
             rope(**b)
     for f, n in ((c.rope, 17), (c.decode, 14), (c.prompt, 9)):
         with pytest.raises(TypeError):
             f(*[0] * (n - 1))
-    with pytest.raises((AttributeError, TypeError)):
+    with pytest.raises(TypeError):
         c.prompt(0, 0, 1, 2, 3, 4, 5, 6, 0.0)
+    with pytest.raises(TypeError):
+        prompt(lse=3)
+    # a tensor without memory of its own raises a C++ error, which comes back as a Python one
+    with pytest.raises((RuntimeError, ValueError)):
+        prompt(cu=torch.sparse_coo_tensor(torch.tensor([[0]]), torch.tensor([1], dtype=i32), (3,), check_invariants=True))
