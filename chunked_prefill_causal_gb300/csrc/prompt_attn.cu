@@ -872,19 +872,20 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
                            tm_q, tm_k, tm_v, p);
 }
 
-// One query tile a CTA, two CTAs per SM, where the second tile of a pair would
-// mostly be absent (sequences of up to T tokens on average: 1024 prompts of 32
-// tokens, 32/8 heads, take 136 us, in pairs 210), and where every tile can have an
-// SM of its own (one prompt of 77 tokens 7.9 us, in pairs 8.8; of 500 tokens 13.8
-// and 15.2).  Otherwise pairs, which read each key tile half as often (32 prompts of
-// 1024 tokens: 302 us against 329; one of 16384: 1437 us against 1994).
+// One query tile a CTA, two CTAs per SM, where sequences have up to one key tile on
+// average, or the tiles occupy up to three fifths of the SMs; otherwise pairs, which
+// read each key tile half as often.  32768 tokens of 32/8 heads in prompts of 32, 64,
+// 96, 128, 192, 256 tokens take 157, 135, 127, 120, 157, 164 us one tile a CTA and 245,
+// 140, 154, 121, 141, 146 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
+// 80, 104, 128 tiles) 6.9, 8.8, 11.0, 13.2, 14.2 and 8.0, 10.0, 11.5, 12.1, 13.6; of
+// 16384 1933 and 1354.
 template <int DQ, int DV>
 cudaError_t launch_prompt_d(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             const PromptParams& p, int num_sms, cudaStream_t stream) {
   if constexpr (DQ <= 128) {  // (three stages of 192 dims do not fit half an SM)
-    const int64_t T = kTileM / (p.heads / p.kv_heads);
-    const int64_t tiles = (p.total / T + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
-    if (p.total <= T * p.batch || tiles <= num_sms)
+    const int64_t tokens = kTileM / (p.heads / p.kv_heads);
+    const int64_t tiles = (p.total / tokens + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
+    if (p.total <= static_cast<int64_t>(kTileN) * p.batch || 5 * tiles <= 3 * num_sms)
       return launch_prompt_t<DQ, DV, false>(tm_q, tm_k, tm_v, p, stream);
   }
   return launch_prompt_t<DQ, DV, true>(tm_q, tm_k, tm_v, p, stream);

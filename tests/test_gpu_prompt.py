@@ -37,12 +37,12 @@ SHAPES = [
 ]
 
 
-# LENS runs with one query tile a CTA in most shapes, four times LENS with pairs of tiles.
-@pytest.mark.parametrize("times", [1, 4])
+# Up to 128 rows a sequence (rows of none among them) run with one query tile a CTA, more with pairs of tiles.
+@pytest.mark.parametrize("times,rest", [(1, 5), (1, 900), (4, 2500)])
 @pytest.mark.parametrize("H,Hkv,dq,dv", SHAPES + [(32, 8, 128, 128), (24, 8, 64, 128)])
-def test_matches_formula(H, Hkv, dq, dv, times):
+def test_matches_formula(H, Hkv, dq, dv, times, rest):
     cu = starts(LENS * times)
-    T = int(cu[-1]) + 5
+    T = int(cu[-1]) + rest
     x = randn((T, H * dq + Hkv * (dq + dv)), 1)
     q, k, v = views(x, H, Hkv, dq, dv)
     out = torch.full((T, H, dv), 7.0, dtype=torch.bfloat16, device=DEV)
@@ -66,11 +66,12 @@ def test_batch_shapes(lens):
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("H,Hkv,d", [(8, 2, 128), (6, 2, 64), (2, 2, 128), (32, 8, 128), (48, 16, 64)])
-def test_neighbours_never_reach_a_result(H, Hkv, d, bad):
+@pytest.mark.parametrize("rest", [9, 1000])
+def test_neighbours_never_reach_a_result(H, Hkv, d, bad, rest):
     """Sequences of hostile values before and behind each good one, and in the rows of no sequence."""
     lens = [30, 100, 40, 129, 10, 200, 3]
     cu = starts(lens)
-    T = int(cu[-1]) + 9
+    T = int(cu[-1]) + rest
     q, k, v = randn((T, H, d), 5), randn((T, Hkv, d), 6), randn((T, Hkv, d), 7)
     good = [1, 3, 5]
     for b in range(len(lens)):
@@ -95,20 +96,21 @@ def test_scale_and_no_lse():
     check_sequences(out, None, q, k, v, cu, d, scale=0.4)
 
 
-def test_invalid_ranges_are_left_out_and_reported():
+@pytest.mark.parametrize("T", [100, 600])
+def test_invalid_ranges_are_left_out_and_reported(T):
     H, Hkv, d = 4, 2, 64
-    q, k, v = randn((100, H, d), 11), randn((100, Hkv, d), 12), randn((100, Hkv, d), 13)
-    for cu in ([0, 40, 30, 100], [0, 40, 60, 200], [-20, 10, 50, 100], [0, 40, 1 << 30, 100]):
-        out = torch.full((100, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    q, k, v = randn((T, H, d), 11), randn((T, Hkv, d), 12), randn((T, Hkv, d), 13)
+    for cu in ([0, 40, 30, T], [0, 40, 60, T + 100], [-20, 10, 50, T], [0, 40, 1 << 30, T]):
+        out = torch.full((T, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
         vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV), out=out)
         assert vpp.vpp_last_device_status() == vpp.VPP_ERR_INVALID, cu
-        rest = torch.ones(100, dtype=torch.bool)
+        rest = torch.ones(T, dtype=torch.bool)
         for lo, hi in zip(cu, cu[1:]):
-            if 0 <= lo <= hi <= 100:
+            if 0 <= lo <= hi <= T:
                 rest[lo:hi] = False
         assert bool((out.cpu()[rest] == 7).all()), cu
     # a valid sequence beside the invalid ones is served
-    cu = [0, 40, 60, 200]
+    cu = [0, 40, 60, T + 100]
     out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV))
     check_sequences(out, None, q, k, v, cu[:3], d)
     assert vpp.vpp_last_device_status() == vpp.VPP_ERR_INVALID
@@ -175,12 +177,13 @@ def test_another_stream():
     assert all(torch.equal(o, want) for o in got)
 
 
-def test_many_ragged_sequences():
+@pytest.mark.parametrize("n,power", [(900, 6), (300, 2)])
+def test_many_ragged_sequences(n, power):
     """More sequences than the work list keeps in registers, of very different lengths, empty ones among them."""
     H, Hkv, d = 8, 4, 64
     g = torch.Generator().manual_seed(30)
-    lens = [int(x) for x in (torch.rand(900, generator=g) ** 6 * 500).long()]
-    lens[17], lens[600], lens[899] = 900, 0, 333
+    lens = [int(x) for x in (torch.rand(n, generator=g) ** power * 500).long()]
+    lens[17], lens[n // 3 * 2], lens[n - 1] = 900, 0, 333
     cu = starts(lens)
     T = int(cu[-1])
     q, k, v = randn((T, H, d), 31), randn((T, Hkv, d), 32), randn((T, Hkv, d), 33)
@@ -191,14 +194,15 @@ def test_many_ragged_sequences():
 
 
 @pytest.mark.parametrize("H,Hkv,d", [(8, 8, 128), (32, 8, 64)])
-def test_few_live_rows_of_many(H, Hkv, d):
+@pytest.mark.parametrize("empty", [0, 300])
+def test_few_live_rows_of_many(H, Hkv, d, empty):
     """A launch sized for many rows of which almost none belong to a sequence."""
     T = 20000
     q, k, v = (torch.full((T, h, d), float("nan"), dtype=torch.bfloat16, device=DEV) for h in (H, Hkv, Hkv))
     live = [randn((70, h, d), 34 + h) for h in (H, Hkv, Hkv)]
     for x, y in zip((q, k, v), live):
         x[5:75] = y.to(DEV)
-    cu = torch.tensor([5, 5, 75, 75], dtype=torch.int32)
+    cu = torch.tensor([5, 5, 75, 75] + [75] * empty, dtype=torch.int32)
     out = torch.full((T, H, d), 7.0, dtype=torch.bfloat16, device=DEV)
     vpp.vpp_prompt_attn(q, k, v, cu.to(DEV), out=out)
     check_sequences(out[5:75], None, *live, [0, 70], d)
