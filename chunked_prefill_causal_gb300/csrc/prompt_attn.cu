@@ -64,6 +64,7 @@ namespace {
 using namespace attn_detail;
 
 constexpr int kEntries = 4;  // items handed out at most (two ahead)
+constexpr int kAskTiles = 6;  // key tiles left of an item when the next one is asked for
 
 // Kv heads of a sequence that go together where not all of them fit into L2.
 constexpr int kHeadGroup = 32;
@@ -318,11 +319,15 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
   const uint32_t tbase = *tmem_slot;
 
   // Item i of this CTA, as one thread (producer, issuer) reads it.
-  auto take = [&](int i, Item* it) {
+  auto read_item = [&](int i, Item* it) {
     if (!mbar_wait(bar(S::B_IF + i % kEntries), (i / kEntries) & 1, p.status, abort_flag)) return false;
     *it = entries[i % kEntries];
-    mbar_arrive(bar(S::B_IE + i % kEntries));
     return it->len > 0;
+  };
+  auto take = [&](int i, Item* it) {
+    if (!read_item(i, it)) return false;
+    mbar_arrive(bar(S::B_IE + i % kEntries));
+    return true;
   };
 
   if (warp < 4) {
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
       uint32_t tmp_phase = 0u, tmp_last = 0u;  // parity of B_TMP's next use; tiles that landed there last
       int n_items = 0;
       Item it;
-      for (int i = 0; ok && take(i, &it); ++i) {
+      for (int i = 0; ok && read_item(i, &it); ++i) {
         const int n = max(it.na, it.nb);
         if (i > 0 && !(ok = mbar_wait(bar(S::B_QE), (i - 1) & 1, p.status, abort_flag))) break;
         const int tiles_q = it.nb > 0 ? 2 : 1;
@@ -351,6 +356,8 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
                         it.start + it.tok0 + x * T);
         n_items = i + 1;
         for (int j = 0; ok && j < n; ++j) {
+          // (the next item is asked for when six tiles are left)
+          if (j == max(0, n - kAskTiles)) mbar_arrive(bar(S::B_IE + i % kEntries));
           for (int part = 0; part < 2; ++part) {  // K, then V
             const int t = 2 * (base + j) + part;
             const int pos = S::tile_pos(t);
@@ -476,12 +483,14 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(S::B_FULL + tb));
         };
-        // Further items are asked for once every role has begun this one, the
-        // next one, or two when this is short (an answer, its sequence and its
-        // first copies take as long as a short item: 1024 prompts of 32 tokens took
-        // 194 us with one ahead, 157 us with two).  Asked for as early as the
-        // entries allow, a CTA holds items that others could have run: three prompts
-        // with 128 heads took 182 us, their CTAs ending 113 to 185 us in, now 152 us.
+        // Further items are asked for once every role has begun this one and its
+        // copies are near its end: the next one, or two when this is short (an
+        // answer, its sequence and its first copies take as long as a short item:
+        // 1024 prompts of 32 tokens took 194 us with one ahead, 157 us with two).  A CTA
+        // that asks earlier holds items that others could have run: one prompt of 2000
+        // tokens took 42.1 us asking at an item's start, 32.7 us with six tiles left, four
+        // of 2048 with 128 heads of 192 dims 627 and 608 us; with one tile left the
+        // latter take 645 us, and three of 720 to 1026 tokens 155 us instead of 152.
         // A short item's own rows come first.
         const bool is_short = n <= 2;
         if (is_short) zero_rows();
