@@ -19,7 +19,12 @@ struct VarlenPlan {
 
 // Launches a kernel that may be placed before the one before it in the stream has
 // ended (programmatic dependent launch); the kernel calls grid_wait() before its
-// first global access.
+// first global access.  It is placed once every CTA of the one before has ended, or
+// called grid_launch_next().  Only the decode kernel calls it, for its own join kernel: a
+// kernel placed between the CTAs of another finds the SM's registers and shared memory
+// in pieces, and CTAs that do not fit then run last, by themselves (decode over an E4M3
+// cache, 471 MB, call after call: 106 us so, 76 us without; append and decode 103 and
+// 82 us, 24 ragged prompts 110 and 107).
 template <typename... A>
 cudaError_t launch_overlapped(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
                               const A&... args) {

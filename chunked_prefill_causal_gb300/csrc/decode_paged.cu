@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
   const int h = blockIdx.x - col * p.kv_heads;
   const int G = p.heads / p.kv_heads;
 
-  grid_launch_next();  // the join kernel may be placed beside this one
+  if (cols > 1) grid_launch_next();  // the join kernel may be placed beside this one
 
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
@@ -710,7 +710,6 @@ __global__ void __launch_bounds__(128) decode_join_kernel(const __grid_constant_
   constexpr int PER = DV / 32;
   __shared__ float so[4][DV];
   __shared__ float2 sml[4];
-  grid_launch_next();
   grid_wait();
   const int c = blockIdx.x, hq = blockIdx.y;
   const JoinDesc d = ws.desc[c];

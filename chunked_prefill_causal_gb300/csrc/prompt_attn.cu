@@ -311,7 +311,6 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
     tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
     tmem_relinquish();
   }
-  grid_launch_next();
   grid_wait();
   tc_fence_before();
   __syncthreads();

@@ -95,8 +95,8 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uin
 // in the stream still runs; it waits here, before its first global access, until
 // that one has completed and its writes are visible.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel in the stream be placed once every CTA has come here (it
-// then waits for the whole grid, if it was launched so at all).
+// Lets the next kernel in the stream be placed once every CTA has come here or ended
+// (it then waits for the whole grid, if it was launched so at all).
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------------------------ fences

@@ -129,7 +129,6 @@ __device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (
 template <bool IL, bool F8>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(const __grid_constant__ RopeParams p,
                                                                               const int tile) {
-  grid_launch_next();
   grid_wait();
   // Thread i of the token's `wide` threads.
   const int wide = kRopeThreads / tile;
