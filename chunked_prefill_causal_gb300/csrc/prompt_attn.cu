@@ -19,8 +19,8 @@
 // 512 moved 1.25 GB for the 0.4 GB that there are.)  Where the keys and values of a
 // sequence's heads together outgrow L2, all its items of 32 heads come before the next
 // 32 heads': two prompts of 4096 tokens, 128 heads of their own keys, 192 dims, take
-// 1102 us, all heads together 1185.  Within L2 it loses: eight of 1024 tokens 399 and
-// 390 us.
+// 1076 us, all heads together 1178; four of 2048 609 and 657.  Within L2 it loses: three
+// of 720 to 1026 tokens 157 and 151 us.
 //
 // Persistent CTAs.  A resident CTA takes over another one of the grid that has not
 // started (cluster launch control), so the items go to whichever SM is free, in
@@ -48,7 +48,7 @@
 // TFLOP/s (83 to 85% of the cuBLAS rate; tensor pipe active 67% of the cycles, issue
 // slots 41%).  Bound by the chain of one item (first loads, first softmax, drain,
 // output: 2.5 us beside its keys) for short ones: 24 prompts of 5 to 2500 tokens take
-// 110 us (950 TFLOP/s, tensor pipe 46%).  At 192 dims the ring holds a K tile, its V
+// 107 us (976 TFLOP/s, tensor pipe 46%).  At 192 dims the ring holds a K tile, its V
 // tile and the next K tile, no more, and each item starts by loading 96 KB of Q: three
 // prompts of 720 to 1026 tokens, 128 heads of their own keys, take 151 us, 2.3 times
 // their bytes' time.
@@ -487,9 +487,9 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
         // answer, its sequence and its first copies take as long as a short item:
         // 1024 prompts of 32 tokens took 194 us with one ahead, 157 us with two).  A CTA
         // that asks earlier holds items that others could have run: one prompt of 2000
-        // tokens took 42.1 us asking at an item's start, 32.7 us with six tiles left, four
-        // of 2048 with 128 heads of 192 dims 627 and 608 us; with one tile left the
-        // latter take 645 us, and three of 720 to 1026 tokens 155 us instead of 152.
+        // tokens takes 41.9 us asking at an item's start, 32.5 us with six tiles left, four
+        // of 2048 with 128 heads of 192 dims 623 and 609 us; with one tile left the
+        // latter take 642 us, and three of 720 to 1026 tokens 155 us instead of 151.
         // A short item's own rows come first.
         const bool is_short = n <= 2;
         if (is_short) zero_rows();
@@ -883,10 +883,10 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
 // One query tile a CTA, two CTAs per SM, where sequences have up to one key tile on
 // average, or the tiles occupy up to three fifths of the SMs; otherwise pairs, which
 // read each key tile half as often.  32768 tokens of 32/8 heads in prompts of 32, 64,
-// 96, 128, 192, 256 tokens take 157, 135, 127, 120, 157, 164 us one tile a CTA and 245,
-// 140, 154, 121, 141, 146 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
-// 80, 104, 128 tiles) 6.9, 8.8, 11.0, 13.2, 14.2 and 8.0, 10.0, 11.5, 12.1, 13.6; of
-// 16384 1933 and 1354.
+// 96, 128, 192, 256 tokens take 157, 135, 127, 120, 158, 163 us one tile a CTA and 247,
+// 140, 155, 121, 140, 144 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
+// 80, 104, 128 tiles) 7.2, 9.0, 11.0, 13.0, 13.2 and 8.2, 10.3, 11.9, 12.3, 13.9; of
+// 16384 1934 and 1345.
 template <int DQ, int DV>
 cudaError_t launch_prompt_d(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             const PromptParams& p, int num_sms, cudaStream_t stream) {

@@ -256,8 +256,8 @@ cudaError_t launch_rope_append(const RopeParams& p, bool interleaved, bool fp8, 
   int tile = 1;
   while (tile < kMaxTile && p.total_q >= static_cast<int64_t>(2 * tile) * kRopeCtas * num_sms) tile *= 2;
   // Tokens of many rows are shared by several CTAs while there are fewer than
-  // kRopeWaves waves of them: 800 tokens of 128 + 128 rows of 192 took 22.6 us with
-  // one CTA a token and 21.7 us with several (256 decode tokens: 6.1 and 5.3 us).
+  // kRopeWaves waves of them: 800 tokens of 128 + 128 rows of 192 take 22.3 us with
+  // one CTA a token and 21.5 us with several (256 decode tokens: 6.1 and 5.0 us).
   const int64_t ctas = (p.total_q + tile - 1) / tile;
   const int pass = kRows * (kRopeThreads / tile / (p.dq / 16));  // rows in flight
   const int passes = ((p.q ? p.heads : 0) + p.kv_heads + pass - 1) / pass;
