@@ -62,10 +62,12 @@ constexpr float kLn2p = 0.69314718055994530942f;
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
 
-// CTAs per SM: three where a stage is small and one group of 8 heads fits 128
-// registers, else two.
+// CTAs per SM: three where a stage is small and the registers of q and O leave room in
+// 128, else two.  (Two groups of heads over an E4M3 cache, 1.2 GB, two and three CTAs:
+// 64/64 dims 361 and 276 us, 128/64 259 and 232, 192/64 226 and 208; 128/128, which
+// spills, 228 and 343.  Over a bf16 cache 64/64 dims take 178 and 182 us.)
 constexpr int ctas_per_sm(int dq, int dv, bool f8, int ng) {
-  return ng == 1 && (dq + dv) * (f8 ? 1 : 2) <= 256 ? 3 : 2;
+  return (ng == 1 || f8) && ng * (dq / 8 + dv / 4) <= 80 && (dq + dv) * (f8 ? 1 : 2) <= 256 ? 3 : 2;
 }
 
 // NG: query heads in groups of 8 (a kv head's G heads fill one or two).
