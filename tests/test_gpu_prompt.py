@@ -244,3 +244,21 @@ def test_heads_in_groups(Hkv, lens):
             # (besides P's rounding, t + 1 products added up in float32)
             check_attention(out[lo + t:lo + t + 1], lse[:, lo + t:lo + t + 1], ref, d, HALF_BF16 + (t + 1) * 2.0 ** -23,
                             f"sequence {b} token {t}")
+
+
+@pytest.mark.parametrize("H,Hkv,dq,dv", [(64, 8, 128, 128), (64, 4, 192, 128)])
+def test_offsets_past_32_bits(H, Hkv, dq, dv):
+    """A sequence at the far end of more than 2^31 elements of queries and of output."""
+    n, T = 300, (1 << 31) // (H * 128) + 400
+    q = torch.zeros((T, H, dq), dtype=torch.bfloat16, device=DEV)
+    k, v = (torch.zeros((T, Hkv, d), dtype=torch.bfloat16, device=DEV) for d in (dq, dv))
+    live = randn((n, H, dq), 50), randn((n, Hkv, dq), 51), randn((n, Hkv, dv), 52)
+    for x, y in zip((q, k, v), live):
+        x[T - n:] = y.to(DEV)
+    cu = torch.tensor([T - n, T], dtype=torch.int32, device=DEV)
+    out = torch.zeros((T, H, dv), dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros((H, T), device=DEV)
+    vpp.vpp_prompt_attn(q, k, v, cu, out=out, lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    check_sequences(out[T - n:], lse[:, T - n:], *live, [0, n], dq)
+    assert not bool(out[:T - n].any()) and not bool(lse[:, :T - n].any())

@@ -233,3 +233,40 @@ def test_far_positions_use_their_own_row():
     check_bf16(kc[1, 63:64], rotate(xk, pos, cs, 0, False), rotate_slack(x, cs), "key")
     assert torch.equal(vc[1, 63].cpu(), xv[0])
     assert not bool(kc[0].any()) and not bool(kc[1, :63].any())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_offsets_past_32_bits(fp8):
+    """Rows at the far end of more than 2^32 elements of queries, into the last block of as large a cache."""
+    H, Hkv, d, n = 64, 8, 128, 70
+    T = (1 << 32) // (H * d) + 100
+    pool = (1 << 32) // (64 * Hkv * d) + 5
+    q = torch.zeros((T, H, d), dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros((T, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    live = [randn((n, h, d), 60 + h) for h in (H, Hkv, 1)]
+    q[T - n:], k[T - n:] = live[0].to(DEV), live[1].to(DEV)
+    v = live[2].expand(n, Hkv, d).contiguous()
+    vd = torch.zeros((T, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    vd[T - n:] = v.to(DEV)
+    kc = torch.zeros((pool, 64, Hkv, d), dtype=torch.uint8 if fp8 else torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    table = torch.tensor([[pool - 1, pool - 3]], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([T - n, T], dtype=torch.int32, device=DEV)
+    cs = cos_sin_table(n, d)
+    scales = (torch.ones(Hkv, device=DEV), torch.ones(Hkv, device=DEV)) if fp8 else ()
+    append = vpp.vpp_rope_append_fp8 if fp8 else vpp.vpp_rope_append
+    append(q, k, vd, cs.to(DEV), kc, vc, *scales, table, cu, None, q_out=q)
+    assert vpp.vpp_last_device_status() == 0
+    pos = torch.arange(n)
+    check_bf16(q[T - n:], rotate(live[0], pos, cs, 0, False), rotate_slack(live[0], cs), "q")
+    got_k = torch.cat([kc[pool - 1], kc[pool - 3, :n - 64]])
+    got_v = torch.cat([vc[pool - 1], vc[pool - 3, :n - 64]])
+    want = rotate(live[1], pos, cs, 0, False)
+    if fp8:
+        got_k, got_v = got_k.view(torch.float8_e4m3fn).double().cpu(), got_v.view(torch.float8_e4m3fn).double().cpu()
+        # half a step of E4M3, or of its subnormals (2^-9 apart)
+        assert bool(((got_k - want).abs() <= HALF_E4M3 * want.abs() + 2.0 ** -10 + 1e-4).all())
+        assert bool(((got_v - v.double()).abs() <= HALF_E4M3 * v.double().abs() + 2.0 ** -10).all())
+    else:
+        check_bf16(got_k, want, rotate_slack(live[1], cs), "key")
+        assert torch.equal(got_v.cpu(), v)

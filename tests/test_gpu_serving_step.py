@@ -128,3 +128,76 @@ def test_prompts_and_decode_agree():
         check_attention(one[b:b + 1], lse1[:, b:b + 1], ref, d, HALF_BF16, "decode")
         check_attention(out[at + n - 1:at + n], lse[:, at + n - 1:at + n], ref, d, HALF_BF16, "prompt")
         at += n
+
+
+def test_a_captured_step_on_forked_streams():
+    """The calls of a step captured on two streams that fork and join, between copies and fills: every call sees what the
+    ones before it wrote, in each of many replays."""
+    H, Hkv, d, B = 16, 4, 128, 6
+    lens = [40, 200, 1, 129, 64, 300]
+    T = sum(lens)
+    cs = cos_sin_table(512, d).to(DEV)
+    x0 = [randn((T, (H + 2 * Hkv) * d), 70 + i).to(DEV) for i in range(3)]
+    x = torch.zeros_like(x0[0])
+    q, k, v = views(x, H, Hkv, d, d)
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).to(DEV)
+    ctx = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    last = (cu[1:] - 1).long()
+    table = torch.randperm(B * 5, generator=torch.Generator().manual_seed(9)).to(torch.int32).view(B, 5).to(DEV)
+    kc = torch.zeros((B * 5, 64, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    qr, kr = torch.empty((T, H, d), dtype=torch.bfloat16, device=DEV), torch.empty((T, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    out, o = torch.empty((T, H, d), dtype=torch.bfloat16, device=DEV), torch.empty((B, H, d), dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(vpp.decode_attn_workspace_size(B, H, Hkv, d, d) + 16, dtype=torch.uint8, device=DEV)
+    ql = torch.empty((B, H, d), dtype=torch.bfloat16, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        kc.zero_()
+        vc.fill_(0)
+        vpp.vpp_rope_append(q, k, v, cs, kc, vc, table, cu, q_out=qr, k_out=kr)
+        side.wait_stream(main)
+        vpp.vpp_prompt_attn(qr, kr, v, cu, out=out)
+        with torch.cuda.stream(side):
+            ql.copy_(qr[last])
+            vpp.vpp_decode_attn(ql, kc, vc, table, ctx, out=o, workspace=ws)
+            vpp.vpp_decode_attn(ql, kc, vc, table, ctx, out=o, workspace=ws)
+        main.wait_stream(side)
+        vpp.vpp_prompt_attn(qr, kr, v, cu, out=out)
+        qr.zero_()
+
+    def run(i):
+        x.copy_(x0[i])
+
+    want = []
+    for i in range(3):
+        run(i)
+        step()
+        torch.cuda.synchronize()
+        want.append((out.clone(), o.clone()))
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.current_stream().wait_stream(warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for i in (0, 1, 2, 1, 0, 2):
+        run(i)
+        out.zero_(), o.zero_()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i][0]) and torch.equal(o, want[i][1])
+    assert vpp.vpp_last_device_status() == 0
+    # and the step itself is right, on the rotated rows as the append wrote them
+    run(2)
+    vpp.vpp_rope_append(q, k, v, cs, kc, vc, table, cu, q_out=qr, k_out=kr)
+    for b, n in enumerate(lens):
+        rows = slice(int(cu[b]), int(cu[b]) + n)
+        ref = attend(qr[rows].cpu(), kr[rows].cpu(), v[rows].cpu(), d ** -0.5, True)
+        check_attention(want[2][0][rows], None, ref, d, HALF_BF16, f"prompt {b}")
+        tail = tuple(t[-1:] if i % 2 == 0 else t[:, -1:] for i, t in enumerate(ref))
+        check_attention(want[2][1][b:b + 1], None, tail, d, HALF_BF16, f"decode row {b}")
