@@ -17,10 +17,10 @@
 // and values run at the same time.  (Ordered by their weight alone, equal prompts
 // read each key from HBM once per tile of queries: 32768 tokens in prompts of
 // 512 moved 1.25 GB for the 0.4 GB that there are.)  Where the keys and values of a
-// sequence's heads together outgrow L2, all its items of 32 heads come before the next
-// 32 heads': two prompts of 4096 tokens, 128 heads of their own keys, 192 dims, take
-// 1076 us, all heads together 1178; four of 2048 609 and 657.  Within L2 it loses: three
-// of 720 to 1026 tokens 157 and 151 us.
+// sequence's heads together take more than half of L2, all its items of 32 heads come
+// before the next 32 heads': with 128 heads of their own keys and 192 dims, two prompts
+// of 4096 tokens take 1072 us, all heads together 1177; four of 2048 612 and 659; three
+// of 720 to 1026 147 and 156.
 //
 // Persistent CTAs.  A resident CTA takes over another one of the grid that has not
 // started (cluster launch control), so the items go to whichever SM is free, in
@@ -50,7 +50,7 @@
 // output: 2.5 us beside its keys) for short ones: 24 prompts of 5 to 2500 tokens take
 // 107 us (976 TFLOP/s, tensor pipe 46%).  At 192 dims the ring holds a K tile, its V
 // tile and the next K tile, no more, and each item starts by loading 96 KB of Q: three
-// prompts of 720 to 1026 tokens, 128 heads of their own keys, take 151 us, 2.3 times
+// prompts of 720 to 1026 tokens, 128 heads of their own keys, take 147 us, 2.2 times
 // their bytes' time.
 #include <algorithm>
 #include <climits>
@@ -66,9 +66,10 @@ using namespace attn_detail;
 constexpr int kEntries = 4;  // items handed out at most (two ahead)
 constexpr int kAskTiles = 6;  // key tiles left of an item when the next one is asked for
 
-// Kv heads of a sequence that go together where not all of them fit into L2.
+// Kv heads of a sequence that go together where all of them would take more than half
+// of L2 (129 MB, which queries and output pass through as well).
 constexpr int kHeadGroup = 32;
-constexpr int64_t kKeptBytes = 100ll << 20;  // of the 129 MB
+constexpr int64_t kKeptBytes = 64ll << 20;
 
 struct Item {
   int start, len;  // the sequence's rows
@@ -88,15 +89,15 @@ struct PShape {
   static constexpr int QBYTES = TILES * NQC * kSubTileBytes;
   static constexpr int SOFTMAX = 128 * TILES;
   static constexpr int THREADS = 128 + SOFTMAX;
-  // 228 KB per SM, 1 KB of it per CTA for the system; 640 bytes for the
+  // 228 KB per SM, 1 KB of it per CTA for the system; 768 bytes for the
   // entries and barriers.
   static constexpr int LIMIT = 228 * 1024 / CTAS - 1024;
-  static constexpr int FIT = (LIMIT - QBYTES - 640) / kSubTileBytes;
+  static constexpr int FIT = (LIMIT - QBYTES - 768) / kSubTileBytes;
   static constexpr int NSLOT = FIT > 12 ? 12 : FIT;
   static constexpr int NB = NSLOT;
   static_assert(NSLOT >= NQC + NVC, "ring must hold one K and one V tile");
-  static constexpr int REGS_LOW = PAIR ? kRegsLow : 48;
-  static constexpr int REGS_HIGH = PAIR ? kRegsHigh : 208;
+  static constexpr int REGS_LOW = PAIR ? kRegsLow : 80;
+  static constexpr int REGS_HIGH = PAIR ? kRegsHigh : 176;
   static_assert(128 * REGS_LOW + SOFTMAX * REGS_HIGH <= THREADS * (PAIR ? 168 : 128), "register split exceeds the launch");
   static constexpr int TMEM_COLS = 256 * TILES;  // S tiles, then O tiles
   static constexpr int PV0 = S::PV0, KP0 = S::KP0;
@@ -104,103 +105,110 @@ struct PShape {
   static constexpr int B_Q = 0, B_QE = 1, B_S = 2, B_P = 4, B_P1 = 6, B_O = 8, B_FINAL = 10, B_END = 12, B_IF = 13,
                        B_IE = B_IF + kEntries, B_FULL = B_IE + kEntries, B_EMPTY = B_FULL + NB, B_TMP = B_EMPTY + NB,
                        B_CLC = B_TMP + NB, NBARS = B_CLC + 1;
-  static constexpr int SMEM = QBYTES + NSLOT * kSubTileBytes + (kEntries + 1) * 32 + NBARS * 8 + 16;
+  static constexpr int SMEM = QBYTES + NSLOT * kSubTileBytes + (kEntries + 1) * 32 + NBARS * 8 + 16 + 32 * 4;
   static_assert(SMEM <= LIMIT && SMEM <= kSmemLimit, "shared memory budget");
   // Tile t of the load order (K_0, V_0, K_1, ...): first ring position and slots.
   __device__ __forceinline__ static int tile_pos(int t) { return S::tile_pos(t); }
   __device__ __forceinline__ static int tile_slots(int t) { return S::tile_slots(t); }
 };
 
-// The work list, by one warp.  Sequences of more than half the items of the
-// longest one left form a class; within it they come in their order.  A lane
-// holds one of 32 sequences; items mostly come in increasing order, so most are
-// found among the 32 at hand, and an earlier one starts the scan over.
+// Items of a sequence of rows [s, e): 0 where the range is not one of the call's rows.
+__device__ __forceinline__ int items_of(const PromptParams& p, int s, int e) {
+  const uint64_t x = static_cast<uint32_t>(e - s + p.item_tokens - 1);
+  return s < 0 || e < s || e > p.total ? 0 : static_cast<int>((x * p.item_mul) >> p.item_shift);
+}
+
+// Length class of a sequence of n > 0 items: from the longest (0) on, powers of two.
+__device__ __forceinline__ int class_of(int n) { return __clz(n); }
+
+// Adds up the items of each class, by all threads of the CTA.  (Compact code: it runs
+// once, and what it takes is fetching it.)
+__device__ __forceinline__ void count_classes(const PromptParams& p, int* sums) {
+#pragma unroll 1
+  for (int64_t b = threadIdx.x; b < p.batch; b += blockDim.x) {
+    const int s = __ldg(p.cu + b), e = __ldg(p.cu + b + 1);
+    const int n = items_of(p, s, e);
+    if (n > 0)
+      atomicAdd(&sums[class_of(n)], n);
+    else if (s != e || s < 0 || e > p.total)  // (by every CTA: which ones start is the hardware's choice)
+      record_status(p.status, kStatusInvalid);
+  }
+}
+
+// The work list, by one warp: the classes from the longest on, the sequences of a
+// class in their order.  A lane holds four of 128 sequences; items mostly come in
+// increasing order, so most are found among those at hand, and an earlier one starts
+// the scan over.  (With 32 at hand, and the classes found by two scans of one warp,
+// 1024 prompts of 32 tokens took 157 us, now 130; 256 of 128 with 8/8 heads 50, now 45.)
 struct Finder {
   const PromptParams& p;
-  int tokens, lane;    // tokens of an item
-  int lo, hi;          // the class: sequences of lo <= items < hi
-  int before, items;   // items of the classes before, and of this one
-  int base, scan;      // first sequence at hand, and the class's items before it
-  int start, len;      // this lane's sequence
-  int n, inc;          // its items (0 outside the class), and with those of the lanes before
-  int total;           // items of all sequences, once known
-  __device__ __forceinline__ Finder(const PromptParams& p_, int tokens_)
-      : p(p_), tokens(tokens_), lane(threadIdx.x & 31), lo(INT_MAX), hi(INT_MAX), before(0), items(0), base(0), scan(0),
-        total(INT_MAX) {}
-  // Items of sequence b; its rows in start and len.
-  __device__ __forceinline__ int read(int b, int* first, int* length) const {
-    const int at = min(b, p.batch - 1);
-    const int s = __ldg(p.cu + at), e = __ldg(p.cu + at + 1);
-    *first = s;
-    *length = e - s;
-    if (b >= p.batch) return 0;
-    if (s < 0 || e < s || e > p.total) {
-      // (by every CTA: which ones start, and which are taken over, is the hardware's choice)
-      record_status(p.status, kStatusInvalid);
-      return 0;
-    }
-    return (e - s + tokens - 1) / tokens;
+  int lane;
+  int upto;          // items of the classes up to this lane's
+  int cls, before;   // the class at hand, items of the ones before it
+  int base, scan;    // first sequence at hand, and the class's items before it
+  int row[5];        // first rows of this lane's sequences and of the one behind
+  int mine, inc;     // its items in the class, and with those of the lanes before
+  __device__ __forceinline__ Finder(const PromptParams& p_, const int* sums)
+      : p(p_), lane(threadIdx.x & 31), cls(-1), before(0), base(0), scan(0) {
+    upto = scan_lanes(sums[lane]);
   }
-  __device__ __forceinline__ void load() {
-    n = read(base + lane, &start, &len);
-    if (n < lo || n >= hi) n = 0;
-    inc = n;
+  __device__ __forceinline__ int scan_lanes(int x) const {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
+    return x;
   }
-  // Goes on to the next class; false behind the last one.
-  __device__ __forceinline__ bool next_class() {
-    before += items;
-    hi = lo;
-    int top = 0, sum = 0, x, y;
-#pragma unroll 1
-    for (int b = lane; b < p.batch + 31 - (p.batch + 31) % 32 + lane; b += 32) {
-      const int m = read(b, &x, &y);
-      if (m < hi) top = max(top, m);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    lo = top / 2 + 1;
-#pragma unroll 1
-    for (int b = lane; b < p.batch + 31 - (p.batch + 31) % 32 + lane; b += 32) {
-      const int m = read(b, &x, &y);
-      if (m >= lo && m < hi) sum += m;
-    }
-    items = __reduce_add_sync(0xffffffffu, sum);
-    base = scan = 0;
-    load();
-    return top > 0;
+  // Items of this lane's sequence j, 0 if it is not of the class.
+  __device__ __forceinline__ int count(int j) const {
+    const int n = items_of(p, row[j], row[j + 1]);
+    return n > 0 && class_of(n) == cls ? n : 0;
+  }
+  __device__ __forceinline__ void load() {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) row[j] = __ldg(p.cu + min(static_cast<int64_t>(base) + 4 * lane + j, static_cast<int64_t>(p.batch)));
+    mine = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine += count(j);
+    inc = scan_lanes(mine);
   }
   // Item i: its sequence's rows and its index in the sequence (the last tokens
   // come first); false when there is no such item.
   __device__ __forceinline__ bool find(int i, int* first, int* length, int* index) {
-    if (i >= total) return false;
-    if (i < before) {
-      lo = hi = INT_MAX;
-      before = items = 0;
-    } else if (i < before + scan) {
+    const uint32_t in = __ballot_sync(0xffffffffu, i < upto);
+    if (!in) return false;
+    const int l = __ffs(in) - 1;
+    const int longer = l > 0 ? __shfl_sync(0xffffffffu, upto, l - 1) : 0;
+    if (cls != l || i < longer + scan) {
+      cls = l;
+      before = longer;
       base = scan = 0;
       load();
     }
-    while (i >= before + items)
-      if (!next_class()) {
-        total = before;
-        return false;
-      }
     const int want = i - before;
     while (true) {
       const uint32_t hit = __ballot_sync(0xffffffffu, want < scan + inc);
       if (hit) {
-        const int l = __ffs(hit) - 1;
-        *first = __shfl_sync(0xffffffffu, start, l);
-        *length = __shfl_sync(0xffffffffu, len, l);
-        *index = scan + __shfl_sync(0xffffffffu, inc, l) - 1 - want;
-        return true;
+        int at = want - (scan + inc - mine), s = 0, len = 0, k = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int n = count(j);
+          if (at >= 0 && at < n) {
+            s = row[j];
+            len = row[j + 1] - s;
+            k = n - 1 - at;
+          }
+          at -= n;
+        }
+        const int from = __ffs(hit) - 1;
+        *first = __shfl_sync(0xffffffffu, s, from);
+        *length = __shfl_sync(0xffffffffu, len, from);
+        *index = __shfl_sync(0xffffffffu, k, from);
+        return *length > 0;
       }
       scan += __shfl_sync(0xffffffffu, inc, 31);
-      base += 32;
+      base += 128;
       if (base >= p.batch) return false;  // (only when the ranges overlap so that the counts overflow)
       load();
     }
@@ -275,6 +283,7 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + S::NBARS);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(tmem_slot + 1);
   volatile int* turn = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  int* sums = reinterpret_cast<int*>(tmem_slot + 4);  // items of the 32 length classes
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   const int warp = threadIdx.x >> 5;
@@ -311,7 +320,10 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
     tmem_alloc(smem_u32(tmem_slot), S::TMEM_COLS);
     tmem_relinquish();
   }
+  if (threadIdx.x >= 32 && threadIdx.x < 64) sums[lane] = 0;
   grid_wait();
+  __syncthreads();
+  count_classes(p, sums);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -403,7 +415,7 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
       }
     } else if (warp == 2) {
       // --------------------------------------- items, and V rows of other sequences
-      Finder finder(p, S::TILES * T);
+      Finder finder(p, sums);
       int requests = 0;
       bool ok = true;
       Item it;
@@ -485,11 +497,11 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
         // Further items are asked for once every role has begun this one and its
         // copies are near its end: the next one, or two when this is short (an
         // answer, its sequence and its first copies take as long as a short item:
-        // 1024 prompts of 32 tokens took 194 us with one ahead, 157 us with two).  A CTA
+        // 1024 prompts of 32 tokens take 164 us with one ahead, 130 us with two).  A CTA
         // that asks earlier holds items that others could have run: one prompt of 2000
-        // tokens takes 41.9 us asking at an item's start, 32.5 us with six tiles left, four
-        // of 2048 with 128 heads of 192 dims 623 and 609 us; with one tile left the
-        // latter take 642 us, and three of 720 to 1026 tokens 155 us instead of 151.
+        // tokens takes 42.6 us asking at an item's start, 32.4 us with six tiles left, four
+        // of 2048 with 128 heads of 192 dims 624 and 612 us; with one tile left the
+        // latter take 649 us.
         // A short item's own rows come first.
         const bool is_short = n <= 2;
         if (is_short) zero_rows();
@@ -860,7 +872,7 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
 
 template <int DQ, int DV, bool PAIR>
 cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                            const PromptParams& p, cudaStream_t stream) {
+                            PromptParams p, cudaStream_t stream) {
   using S = PShape<DQ, DV, PAIR>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -873,9 +885,15 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
   }
   // Items: at most one for each whole tile (pair) of the rows and one partial
   // one for each sequence.
-  const int64_t tokens = S::TILES * (kTileM / (p.heads / p.kv_heads));
+  const int tokens = S::TILES * (kTileM / (p.heads / p.kv_heads));
   const int64_t items = (p.total / tokens + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
   if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
+  // x / tokens = x * mul >> shift, exact while x (2^30 + 255 at most) times the excess
+  // of mul * tokens over 2^shift (below tokens) is less than 2^shift
+  p.item_tokens = tokens;
+  p.item_shift = 30;
+  while (1 << (p.item_shift - 30) < tokens) ++p.item_shift;
+  p.item_mul = ((1ull << p.item_shift) + tokens - 1) / tokens;
   return launch_overlapped(prompt_attn_kernel<DQ, DV, PAIR>, dim3(static_cast<unsigned>(items)), S::THREADS, S::SMEM, stream,
                            tm_q, tm_k, tm_v, p);
 }
@@ -883,10 +901,10 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
 // One query tile a CTA, two CTAs per SM, where sequences have up to one key tile on
 // average, or the tiles occupy up to three fifths of the SMs; otherwise pairs, which
 // read each key tile half as often.  32768 tokens of 32/8 heads in prompts of 32, 64,
-// 96, 128, 192, 256 tokens take 157, 135, 127, 120, 158, 163 us one tile a CTA and 247,
-// 140, 155, 121, 140, 144 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
-// 80, 104, 128 tiles) 7.2, 9.0, 11.0, 13.0, 13.2 and 8.2, 10.3, 11.9, 12.3, 13.9; of
-// 16384 1934 and 1345.
+// 96, 128, 192, 256 tokens take 130, 125, 123, 120, 164, 169 us one tile a CTA and 221,
+// 128, 148, 116, 142, 146 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
+// 80, 104, 128 tiles) 7.2, 9.3, 11.1, 13.0, 13.2 and 8.4, 10.5, 11.9, 12.6, 13.9; of
+// 16384 1927 and 1349.
 template <int DQ, int DV>
 cudaError_t launch_prompt_d(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             const PromptParams& p, int num_sms, cudaStream_t stream) {
