@@ -247,8 +247,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
     total += scan[w];
   }
   const int nc = min(cols, total);  // columns with pages: at least one page each
-  const int first = col < nc ? static_cast<int>(static_cast<int64_t>(col) * total / nc) : 0;
-  const int last = col < nc ? static_cast<int>(static_cast<int64_t>(col + 1) * total / nc) : 0;  // one past
+  // first page of column c: c total / nc, in 32 bits
+  const uint32_t un = max(nc, 1), share = static_cast<uint32_t>(total) / un, extra = total - share * un;
+  auto first_page = [&](uint32_t c) { return static_cast<int>(c * share + c * extra / un); };
+  const int first = col < nc ? first_page(col) : 0;
+  const int last = col < nc ? first_page(col + 1) : 0;  // one past
   __syncthreads();
   if (first < last && first >= before && first < before + sum) {
     int at = before;
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
       JoinDesc d{-1, 0, 0, 0};
       if (n_pages > 0 && start_page > 0) {
         const int begin = first - start_page;  // the sequence's first page
-        const int prev = static_cast<int>(static_cast<int64_t>(col - 1) * total / nc);
+        const int prev = first_page(col - 1);
         if (begin >= prev) {
           const int64_t end = begin + pages_of(valid_ctx(p, __ldg(p.ctx + start_b)));  // one past
           const int last_col = static_cast<int>((end * nc - 1) / total);
