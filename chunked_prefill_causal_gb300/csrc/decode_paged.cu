@@ -11,7 +11,7 @@
 // query heads of its kv head only.  Measured on a GB300 (copy bandwidth 6.78 TB/s):
 // 256 sequences of 1024 to 32768 tokens, 8 kv heads of 128, 16.6 GB in 2.35 ms
 // (7.05 TB/s); 200 over an E4M3 cache 6.75 TB/s; one of 131071 tokens, 537 MB, in
-// 84 us (6.4 TB/s).  One of 1000 tokens takes 6.8 us, the latency of two launches
+// 83 us (6.45 TB/s).  One of 1000 tokens takes 6.8 us, the latency of two launches
 // and of lengths -> block table -> page -> softmax -> join.
 //
 // Work split.  The pages (64-token blocks) of all sequences, in order, form

@@ -17,7 +17,7 @@
 // Bound by HBM for many tokens (each input is read and each output written
 // once), by the latency of the chain lengths -> block and table row -> stores
 // for few.  Measured on a GB300: 16384 tokens of 64 + 8 heads of 128, 679 MB,
-// in 104.4 us (6.5 TB/s, 96% of the copy bandwidth); 4 decode tokens in 2.8 us.
+// in 103.7 us (6.55 TB/s, 97% of the copy bandwidth); 4 decode tokens in 2.5 us.
 //
 // Work split.  A row (one head of one token) is d / 16 tasks of two 16-byte
 // vectors: eight pairs of the rotated dims (both ends of the pairs, so that one
@@ -25,7 +25,8 @@
 // A token is served by 64 threads of a CTA, or by all 256 when there are few
 // tokens.  A thread keeps its task for every row of the token, so the eight
 // cosines and sines are loaded once for all heads; two rows are in flight at
-// once, the first ones while the token's position and slot are looked up.
+// once, the first ones while the token's position is looked up, and the angles load
+// beside the block-table entry (one after the other: 2.8 us for the 4 tokens).
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -71,45 +72,39 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// Where a token goes: its position (-1: padding or invalid) and cache row.
+// Where a token belongs: its sequence and its position there (-1: padding or invalid).
 struct Place {
-  int64_t row;
+  int32_t b;
   int32_t pos;
 };
 
 __device__ __forceinline__ Place place_of(const RopeParams& p, int64_t t) {
-  // A decode batch has one token per sequence: try sequence t first.
+  // A decode batch has one token per sequence: try sequence t first, its length
+  // loaded beside its rows.
   int b = -1;
-  int64_t lo = 0, hi = 0;
+  int64_t lo = 0, hi = 0, ctx = 0;
   if (t < p.batch) {
     lo = __ldg(p.cu + t);
     hi = __ldg(p.cu + t + 1);
+    if (p.ctx) ctx = __ldg(p.ctx + t);
     if (lo <= t && t < hi) b = static_cast<int>(t);
   }
   if (b < 0) {
     b = find_seq(p.cu, p.batch, t);
     lo = __ldg(p.cu + b);
     hi = __ldg(p.cu + b + 1);
+    if (p.ctx) ctx = __ldg(p.ctx + b);
   }
   if (t < lo || t >= hi) return Place{0, -1};
-  const int64_t ctx = p.ctx ? __ldg(p.ctx + b) : hi - lo;
+  if (!p.ctx) ctx = hi - lo;
   if (ctx == 0) return Place{0, -1};
   const int64_t pos = ctx - (hi - t);
-  bool ok = ctx >= hi - lo && pos >= 0 && (p.rot_dim == 0 || pos < p.table_rows);
-  int64_t row = 0;
-  if (ok && p.k_cache) {
-    ok = pos / kBlockTokens < p.max_blocks_per_seq;
-    if (ok) {
-      const int32_t blk = __ldg(p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq + pos / kBlockTokens);
-      ok = blk >= 0 && blk < p.num_blocks;
-      row = static_cast<int64_t>(blk) * kBlockTokens + pos % kBlockTokens;
-    }
-  }
-  if (!ok) {
+  if (ctx < hi - lo || pos < 0 || (p.rot_dim > 0 && pos >= p.table_rows) ||
+      (p.k_cache && pos / kBlockTokens >= p.max_blocks_per_seq)) {
     record_status(p.status, kStatusInvalid);
     return Place{0, -1};
   }
-  return Place{row, static_cast<int32_t>(pos)};
+  return Place{b, static_cast<int32_t>(pos)};
 }
 
 // Rotates the eight pairs of a task in float32.
@@ -157,6 +152,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
   const uint16_t* qs = p.q + t * p.q_stride;
   const uint16_t* ks = p.k + t * p.k_stride - static_cast<int64_t>(hq) * p.dq;
   uint4 a[kRows], b[kRows];
+  float scales[kRows];
   auto load = [&](int r0) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
@@ -165,6 +161,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
         const uint16_t* src = (r < hq ? qs : ks) + r * p.dq;
         a[j] = ld_once(src + d0);
         b[j] = ld_once(src + d1);
+        if (F8 && r >= hq) scales[j] = __ldg(p.k_scale + r - hq);
       }
     }
   };
@@ -175,6 +172,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
   if (t == 0 && i == 0 && blockIdx.y == 0 && __ldg(p.cu + p.batch) > p.total_q) record_status(p.status, kStatusInvalid);
   const Place at = place_of(p, t);
   if (at.pos < 0) return;
+  // the angles load beside the block
+  int32_t blk = 0;
+  if (p.k_cache)
+    blk = __ldg(p.block_table + static_cast<int64_t>(at.b) * p.max_blocks_per_seq + at.pos / kBlockTokens);
   float cs[8], sn[8];
   if (angle >= 0) {
     const float* src = p.cos_sin + static_cast<int64_t>(at.pos) * p.rot_dim + angle;
@@ -186,6 +187,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
       sn[e] = y.x; sn[e + 1] = y.y; sn[e + 2] = y.z; sn[e + 3] = y.w;
     }
   }
+  if (p.k_cache && (blk < 0 || blk >= p.num_blocks)) {
+    record_status(p.status, kStatusInvalid);
+    return;
+  }
+  const int64_t slot = static_cast<int64_t>(blk) * kBlockTokens + at.pos % kBlockTokens;
   for (int r0 = begin; r0 < rows; r0 += stride) {
     if (r0 != begin) load(r0);
 #pragma unroll
@@ -210,10 +216,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
         put(p.q_out + t * p.q_out_stride + r * p.dq);
       } else {
         const int h = r - hq;
-        const int64_t row = (at.row * p.kv_heads + h) * p.dq;
+        const int64_t row = (slot * p.kv_heads + h) * p.dq;
         if (p.k_out) put(p.k_out + t * p.k_out_stride + h * p.dq);
         if (F8) {
-          const float scale = __ldg(p.k_scale + h);
+          const float scale = scales[j];
           uint8_t* dst = static_cast<uint8_t*>(p.k_cache) + row;
           *reinterpret_cast<uint2*>(dst + d0) = codes8(x, scale);
           *reinterpret_cast<uint2*>(dst + d1) = codes8(y, scale);
@@ -226,13 +232,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
   if (!p.k_cache) return;
   // values: the token's kv heads are contiguous on both sides
   const uint16_t* vs = p.v + t * p.v_stride;
-  const int64_t row = at.row * p.kv_heads * p.dv;
+  const int64_t row = slot * p.kv_heads * p.dv;
   const int n = p.kv_heads * p.dv / 8;
   for (int e0 = i + blockIdx.y * 2 * kRows * wide; e0 < n; e0 += gridDim.y * 2 * kRows * wide) {
     uint4 w[2 * kRows];
+    float scale[2 * kRows];
 #pragma unroll
     for (int j = 0; j < 2 * kRows; ++j)
-      if (e0 + j * wide < n) w[j] = ld_once(vs + 8 * (e0 + j * wide));
+      if (e0 + j * wide < n) {
+        w[j] = ld_once(vs + 8 * (e0 + j * wide));
+        if (F8) scale[j] = __ldg(p.v_scale + 8 * (e0 + j * wide) / p.dv);
+      }
 #pragma unroll
     for (int j = 0; j < 2 * kRows; ++j) {
       const int e = e0 + j * wide;
@@ -241,7 +251,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rope_append_kernel(co
         float x[8];
         unpack8(w[j], x);
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + row + 8 * e) =
-            codes8(x, __ldg(p.v_scale + 8 * e / p.dv));
+            codes8(x, scale[j]);
       } else {
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.v_cache) + row + 8 * e) = w[j];
       }
@@ -257,7 +267,7 @@ cudaError_t launch_rope_append(const RopeParams& p, bool interleaved, bool fp8, 
   while (tile < kMaxTile && p.total_q >= static_cast<int64_t>(2 * tile) * kRopeCtas * num_sms) tile *= 2;
   // Tokens of many rows are shared by several CTAs while there are fewer than
   // kRopeWaves waves of them: 800 tokens of 128 + 128 rows of 192 take 22.3 us with
-  // one CTA a token and 21.5 us with several (256 decode tokens: 6.1 and 5.0 us).
+  // one CTA a token and 21.5 us with several (256 decode tokens: 6.1 and 5.1 us).
   const int64_t ctas = (p.total_q + tile - 1) / tile;
   const int pass = kRows * (kRopeThreads / tile / (p.dq / 16));  // rows in flight
   const int passes = ((p.q ? p.heads : 0) + p.kv_heads + pass - 1) / pass;
