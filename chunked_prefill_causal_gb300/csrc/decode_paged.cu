@@ -10,8 +10,8 @@
 // Bound by HBM: every cached key and value is read once and used for the G
 // query heads of its kv head only.  Measured on a GB300 (copy bandwidth 6.78 TB/s):
 // 256 sequences of 1024 to 32768 tokens, 8 kv heads of 128, 16.6 GB in 2.35 ms
-// (7.05 TB/s); 200 over an E4M3 cache 6.75 TB/s; one of 131071 tokens, 537 MB, in
-// 83 us (6.45 TB/s).  One of 1000 tokens takes 6.8 us, the latency of two launches
+// (7.05 TB/s); 200 over an E4M3 cache 6.8 TB/s; one of 131071 tokens, 537 MB, in
+// 84 us (6.4 TB/s).  One of 1000 tokens takes 6.3 us, the latency of two launches
 // and of lengths -> block table -> page -> softmax -> join.
 //
 // Work split.  The pages (64-token blocks) of all sequences, in order, form
@@ -162,6 +162,12 @@ __device__ __forceinline__ int valid_ctx(const PagedDecodeParams& p, int ctx) {
 }
 __device__ __forceinline__ int pages_of(int ctx) { return (ctx + kBlockTokens - 1) / kBlockTokens; }
 
+// First page of column c: c total / nc, in 32 bits.
+__device__ __forceinline__ int first_page(uint32_t c, uint32_t total, uint32_t nc) {
+  const uint32_t share = total / nc, extra = total - share * nc;
+  return static_cast<int>(c * share + c * extra / nc);
+}
+
 // Walks the non-empty sequences from one on; every lane of the warp holds one
 // of 32 lengths, so a run of empty rows costs one load per 32.
 struct SeqWalk {
@@ -226,58 +232,83 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
     fence_mbar_init();
   }
   grid_wait();
-  // ---- this column's pages: warp w adds up the w-th fifth of the sequences,
-  // and the one whose range holds the column's first page finds it.
-  const int per = (p.batch + 4) / 5;
-  const int b0 = min(p.batch, warp * per), b1 = min(p.batch, b0 + per);
-  int sum = 0;
-  for (int b = b0 + lane; b < b1; b += 32) {
-    const int raw = __ldg(p.ctx + b);
-    const int c = valid_ctx(p, raw);
+  // ---- this column's pages
+  int total, nc, first, last, start_b = 0, start_page = 0;  // start_page: pages of start_b before this column
+  auto share_out = [&]() {
+    nc = min(cols, total);  // columns with pages: at least one page each
+    first = col < nc ? first_page(col, total, nc) : 0;
+    last = col < nc ? first_page(col + 1, total, nc) : 0;  // one past
+  };
+  auto pages_at = [&](int b, int end) {  // (an invalid length counts as 0 and is recorded once)
+    if (b >= end) return 0;
+    const int raw = __ldg(p.ctx + b), c = valid_ctx(p, raw);
     if (c != raw && blockIdx.x == 0) record_status(p.status, kStatusInvalid);
-    sum += pages_of(c);
-  }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) scan[warp] = sum;
-  __syncthreads();
-  int before = 0, total = 0;
+    return pages_of(c);
+  };
+  // Looks for the page `first` in the lanes' sequences, from `from` on, with `at` pages
+  // before them.
+  auto locate = [&](int from, int n, int inc, int at) {
+    const uint32_t hit = __ballot_sync(0xffffffffu, first < at + inc);
+    if (!hit) return false;
+    const int l = __ffs(hit) - 1;
+    start_b = from + l;
+    start_page = first - __shfl_sync(0xffffffffu, at + inc - n, l);
+    return true;
+  };
+  auto prefix = [&](int n) {  // inclusive, over the lanes
 #pragma unroll
-  for (int w = 0; w < 5; ++w) {
-    if (w < warp) before += scan[w];
-    total += scan[w];
-  }
-  const int nc = min(cols, total);  // columns with pages: at least one page each
-  // first page of column c: c total / nc, in 32 bits
-  const uint32_t un = max(nc, 1), share = static_cast<uint32_t>(total) / un, extra = total - share * un;
-  auto first_page = [&](uint32_t c) { return static_cast<int>(c * share + c * extra / un); };
-  const int first = col < nc ? first_page(col) : 0;
-  const int last = col < nc ? first_page(col + 1) : 0;  // one past
-  __syncthreads();
-  if (first < last && first >= before && first < before + sum) {
-    int at = before;
-    for (int b = b0;; b += 32) {
-      const int n = b + lane < b1 ? pages_of(valid_ctx(p, __ldg(p.ctx + b + lane))) : 0;
-      int inc = n;  // inclusive prefix over the lanes
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, n, o);
+      if (lane >= o) n += y;
+    }
+    return n;
+  };
+  if (p.batch <= 32) {
+    // every warp finds it by itself (one row of 1000 keys 6.8 -> 6.3 us)
+    const int n = pages_at(lane, p.batch), inc = prefix(n);
+    total = __shfl_sync(0xffffffffu, inc, 31);
+    share_out();
+    if (first < last) locate(0, n, inc, 0);
+    __syncthreads();  // the barriers are set up
+  } else {
+    // warp w adds up the w-th fifth of the sequences, and the one whose range holds
+    // the column's first page finds it
+    const int per = (p.batch + 4) / 5;
+    const int b0 = min(p.batch, warp * per), b1 = min(p.batch, b0 + per);
+    int sum = 0;
+    for (int b = b0; b < b1; b += 32) sum += pages_at(b + lane, b1);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) scan[warp] = sum;
+    __syncthreads();
+    int before = 0;
+    total = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+    for (int w = 0; w < 5; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    share_out();
+    __syncthreads();
+    if (first < last && first >= before && first < before + sum) {
+      int at = before;
+      for (int b = b0;; b += 32) {
+        const int n = b + lane < b1 ? pages_of(valid_ctx(p, __ldg(p.ctx + b + lane))) : 0;
+        const int inc = prefix(n);
+        if (locate(b, n, inc, at)) break;
+        at += __shfl_sync(0xffffffffu, inc, 31);
       }
-      const uint32_t hit = __ballot_sync(0xffffffffu, first < at + inc);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          scan[5] = b + lane;
-          scan[6] = first - (at + inc - n);
-        }
-        break;
+      if (lane == 0) {
+        scan[5] = start_b;
+        scan[6] = start_page;
       }
-      at += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    __syncthreads();
+    if (first < last) {
+      start_b = scan[5];
+      start_page = scan[6];
     }
   }
-  __syncthreads();
   const int n_pages = last - first;
-  const int start_b = n_pages > 0 ? scan[5] : 0;
-  const int start_page = n_pages > 0 ? scan[6] : 0;  // pages of start_b before this column
 
   if (warp == kConsumers) {
     // ------------------------------------------------------ producer
@@ -287,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
       JoinDesc d{-1, 0, 0, 0};
       if (n_pages > 0 && start_page > 0) {
         const int begin = first - start_page;  // the sequence's first page
-        const int prev = first_page(col - 1);
+        const int prev = first_page(col - 1, total, nc);
         if (begin >= prev) {
           const int64_t end = begin + pages_of(valid_ctx(p, __ldg(p.ctx + start_b)));  // one past
           const int last_col = static_cast<int>((end * nc - 1) / total);
