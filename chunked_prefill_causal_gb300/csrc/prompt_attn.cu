@@ -112,10 +112,14 @@ struct PShape {
   __device__ __forceinline__ static int tile_slots(int t) { return S::tile_slots(t); }
 };
 
+// x / d, with d's multiplier and shift from the host (see divide_by()).
+__device__ __forceinline__ int quotient(uint32_t x, uint64_t mul, int shift) {
+  return static_cast<int>((x * mul) >> shift);
+}
+
 // Items of a sequence of rows [s, e): 0 where the range is not one of the call's rows.
 __device__ __forceinline__ int items_of(const PromptParams& p, int s, int e) {
-  const uint64_t x = static_cast<uint32_t>(e - s + p.item_tokens - 1);
-  return s < 0 || e < s || e > p.total ? 0 : static_cast<int>((x * p.item_mul) >> p.item_shift);
+  return s < 0 || e < s || e > p.total ? 0 : quotient(e - s + p.item_tokens - 1, p.item_mul, p.item_shift);
 }
 
 // Length class of a sequence of n > 0 items: from the longest (0) on, powers of two.
@@ -146,8 +150,8 @@ struct Finder {
   int upto;          // items of the classes up to this lane's
   int cls, before;   // the class at hand, items of the ones before it
   int base, scan;    // first sequence at hand, and the class's items before it
-  int row[5];        // first rows of this lane's sequences and of the one behind
-  int mine, inc;     // its items in the class, and with those of the lanes before
+  int row[5], n[4];  // this lane's sequences: first rows (and that behind), items in the class
+  int mine, inc;     // their sum, and with those of the lanes before
   __device__ __forceinline__ Finder(const PromptParams& p_, const int* sums)
       : p(p_), lane(threadIdx.x & 31), cls(-1), before(0), base(0), scan(0) {
     upto = scan_lanes(sums[lane]);
@@ -160,17 +164,17 @@ struct Finder {
     }
     return x;
   }
-  // Items of this lane's sequence j, 0 if it is not of the class.
-  __device__ __forceinline__ int count(int j) const {
-    const int n = items_of(p, row[j], row[j + 1]);
-    return n > 0 && class_of(n) == cls ? n : 0;
-  }
   __device__ __forceinline__ void load() {
 #pragma unroll
-    for (int j = 0; j < 5; ++j) row[j] = __ldg(p.cu + min(static_cast<int64_t>(base) + 4 * lane + j, static_cast<int64_t>(p.batch)));
+    for (int j = 0; j < 5; ++j)
+      row[j] = __ldg(p.cu + min(static_cast<int64_t>(base) + 4 * lane + j, static_cast<int64_t>(p.batch)));
     mine = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) mine += count(j);
+    for (int j = 0; j < 4; ++j) {
+      const int m = items_of(p, row[j], row[j + 1]);
+      n[j] = m > 0 && class_of(m) == cls ? m : 0;
+      mine += n[j];
+    }
     inc = scan_lanes(mine);
   }
   // Item i: its sequence's rows and its index in the sequence (the last tokens
@@ -190,26 +194,24 @@ struct Finder {
     while (true) {
       const uint32_t hit = __ballot_sync(0xffffffffu, want < scan + inc);
       if (hit) {
-        int at = want - (scan + inc - mine), s = 0, len = 0, k = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int n = count(j);
-          if (at >= 0 && at < n) {
-            s = row[j];
-            len = row[j + 1] - s;
-            k = n - 1 - at;
-          }
-          at -= n;
-        }
         const int from = __ffs(hit) - 1;
+        int at = want - (scan + inc - mine), s = row[0], e = row[1], m = n[0];
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+          if (at >= m) {
+            at -= m;
+            s = row[j];
+            e = row[j + 1];
+            m = n[j];
+          }
         *first = __shfl_sync(0xffffffffu, s, from);
-        *length = __shfl_sync(0xffffffffu, len, from);
-        *index = __shfl_sync(0xffffffffu, k, from);
-        return *length > 0;
+        *length = __shfl_sync(0xffffffffu, at >= 0 && at < m ? e - s : 0, from);
+        *index = __shfl_sync(0xffffffffu, m - 1 - at, from);
+        return *length > 0;  // (always, unless the ranges overlap so that the counts overflow)
       }
       scan += __shfl_sync(0xffffffffu, inc, 31);
       base += 128;
-      if (base >= p.batch) return false;  // (only when the ranges overlap so that the counts overflow)
+      if (base >= p.batch) return false;  // (likewise)
       load();
     }
   }
@@ -294,26 +296,19 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
   if (threadIdx.x == 0) {
     *abort_flag = 0u;
     *turn = 0;
-    mbar_init(bar(S::B_Q), 1);
-    mbar_init(bar(S::B_CLC), 1);
-    mbar_init(bar(S::B_QE), S::TILES);
-    for (int x = 0; x < 2; ++x) {
-      mbar_init(bar(S::B_S + x), 1);
-      mbar_init(bar(S::B_P + x), 128);
-      mbar_init(bar(S::B_P1 + x), 128);
-      mbar_init(bar(S::B_O + x), 1);
-      mbar_init(bar(S::B_FINAL + x), 1);
-    }
-    mbar_init(bar(S::B_END), 5 * S::TILES);  // the softmax warps and the MMA issuers
-    for (int i = 0; i < kEntries; ++i) {
-      mbar_init(bar(S::B_IF + i), 1);
-      mbar_init(bar(S::B_IE + i), 1 + 5 * S::TILES);  // producer, issuers, softmax warps
-    }
-    for (int i = 0; i < S::NB; ++i) {
-      mbar_init(bar(S::B_FULL + i), 1);
-      mbar_init(bar(S::B_EMPTY + i), S::TILES);  // released by the MMA issuers
-      mbar_init(bar(S::B_TMP + i), 1);
-    }
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (threadIdx.x < S::NBARS) {
+    const int i = threadIdx.x;
+    int count = 1;
+    if (i == S::B_QE) count = S::TILES;
+    if (i >= S::B_P && i < S::B_O) count = 128;
+    if (i == S::B_END) count = 5 * S::TILES;                            // the softmax warps and the MMA issuers
+    if (i >= S::B_IE && i < S::B_FULL) count = 1 + 5 * S::TILES;        // producer, issuers, softmax warps
+    if (i >= S::B_EMPTY && i < S::B_TMP) count = S::TILES;              // released by the MMA issuers
+    mbar_init(bar(i), count);
     fence_mbar_init();
   }
   if (warp == 2) {
@@ -345,9 +340,6 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
     regs_dec<S::REGS_LOW>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer
-      tma_prefetch_desc(&tm_q);
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
       bool ok = true;
       int base = 0;    // tile pairs (K and V) of the items before
       int issued = 0;  // tiles whose loads were started
@@ -421,7 +413,7 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
       Item it;
       // Item of CTA `idx`; false if it has none (the grid's size is an upper bound).
       auto item_of = [&](int idx) {
-        const int item = idx / p.kv_heads;
+        const int item = quotient(idx, p.head_mul, p.head_shift);
         int index;
         if (!finder.find(item, &it.start, &it.len, &index)) return false;
         it.g = idx - item * p.kv_heads;
@@ -870,6 +862,15 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
   }
 }
 
+// x / d = x * mul >> shift, with 2^shift at least 2^30 d: exact while x times the excess
+// of mul * d over 2^shift, which is below d, is less than 2^shift; that holds for x up to
+// 2^30 + 512 and every d up to 1024.
+void divide_by(int d, uint64_t* mul, int32_t* shift) {
+  *shift = 30;
+  while (1 << (*shift - 30) < d) ++*shift;
+  *mul = ((1ull << *shift) + d - 1) / d;
+}
+
 template <int DQ, int DV, bool PAIR>
 cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             PromptParams p, cudaStream_t stream) {
@@ -888,12 +889,9 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
   const int tokens = S::TILES * (kTileM / (p.heads / p.kv_heads));
   const int64_t items = (p.total / tokens + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
   if (items > INT32_MAX / 2) return cudaErrorInvalidValue;
-  // x / tokens = x * mul >> shift, exact while x (2^30 + 255 at most) times the excess
-  // of mul * tokens over 2^shift (below tokens) is less than 2^shift
   p.item_tokens = tokens;
-  p.item_shift = 30;
-  while (1 << (p.item_shift - 30) < tokens) ++p.item_shift;
-  p.item_mul = ((1ull << p.item_shift) + tokens - 1) / tokens;
+  divide_by(tokens, &p.item_mul, &p.item_shift);
+  divide_by(p.kv_heads, &p.head_mul, &p.head_shift);
   return launch_overlapped(prompt_attn_kernel<DQ, DV, PAIR>, dim3(static_cast<unsigned>(items)), S::THREADS, S::SMEM, stream,
                            tm_q, tm_k, tm_v, p);
 }

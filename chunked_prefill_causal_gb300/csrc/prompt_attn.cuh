@@ -20,9 +20,9 @@ struct PromptParams {
   int32_t kv_heads;
   float scale_log2;    // softmax scale * log2(e)
   int* status;
-  // (set by the launcher) tokens of an item, and the division by them
-  int32_t item_tokens, item_shift;
-  uint64_t item_mul;
+  // (set by the launcher) tokens of an item, and divisions by them and by kv_heads
+  int32_t item_tokens, item_shift, head_shift;
+  uint64_t item_mul, head_mul;
 };
 
 // Query rows of a tile: kTileM / G tokens of the G heads of a kv head.
