@@ -19,8 +19,8 @@
 // 512 moved 1.25 GB for the 0.4 GB that there are.)  Where the keys and values of a
 // sequence's heads together take more than half of L2, all its items of 32 heads come
 // before the next 32 heads': with 128 heads of their own keys and 192 dims, two prompts
-// of 4096 tokens take 1072 us, all heads together 1177; four of 2048 612 and 659; three
-// of 720 to 1026 147 and 156.
+// of 4096 tokens take 1068 us, all heads together 1172; four of 2048 604 and 654; three
+// of 720 to 1026 146 and 154.
 //
 // Persistent CTAs.  A resident CTA takes over another one of the grid that has not
 // started (cluster launch control), so the items go to whichever SM is free, in
@@ -48,9 +48,9 @@
 // TFLOP/s (83 to 85% of the cuBLAS rate; tensor pipe active 67% of the cycles, issue
 // slots 41%).  Bound by the chain of one item (first loads, first softmax, drain,
 // output: 2.5 us beside its keys) for short ones: 24 prompts of 5 to 2500 tokens take
-// 107 us (976 TFLOP/s, tensor pipe 46%).  At 192 dims the ring holds a K tile, its V
+// 106 us (984 TFLOP/s, tensor pipe 46%).  At 192 dims the ring holds a K tile, its V
 // tile and the next K tile, no more, and each item starts by loading 96 KB of Q: three
-// prompts of 720 to 1026 tokens, 128 heads of their own keys, take 147 us, 2.2 times
+// prompts of 720 to 1026 tokens, 128 heads of their own keys, take 146 us, 2.2 times
 // their bytes' time.
 #include <algorithm>
 #include <climits>
@@ -143,7 +143,7 @@ __device__ __forceinline__ void count_classes(const PromptParams& p, int* sums) 
 // class in their order.  A lane holds four of 128 sequences; items mostly come in
 // increasing order, so most are found among those at hand, and an earlier one starts
 // the scan over.  (With 32 at hand, and the classes found by two scans of one warp,
-// 1024 prompts of 32 tokens took 157 us, now 130; 256 of 128 with 8/8 heads 50, now 45.)
+// 1024 prompts of 32 tokens took 157 us, now 126; 256 of 128 with 8/8 heads 50, now 45.)
 struct Finder {
   const PromptParams& p;
   int lane;
@@ -489,11 +489,11 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
         // Further items are asked for once every role has begun this one and its
         // copies are near its end: the next one, or two when this is short (an
         // answer, its sequence and its first copies take as long as a short item:
-        // 1024 prompts of 32 tokens take 164 us with one ahead, 130 us with two).  A CTA
+        // 1024 prompts of 32 tokens take 156 us with one ahead, 126 us with two).  A CTA
         // that asks earlier holds items that others could have run: one prompt of 2000
-        // tokens takes 42.6 us asking at an item's start, 32.4 us with six tiles left, four
-        // of 2048 with 128 heads of 192 dims 624 and 612 us; with one tile left the
-        // latter take 649 us.
+        // tokens takes 41.2 us asking at an item's start, 32.4 us with six tiles left, four
+        // of 2048 with 128 heads of 192 dims 616 and 604 us; with one tile left the
+        // latter take 640 us.
         // A short item's own rows come first.
         const bool is_short = n <= 2;
         if (is_short) zero_rows();
@@ -899,10 +899,10 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
 // One query tile a CTA, two CTAs per SM, where sequences have up to one key tile on
 // average, or the tiles occupy up to three fifths of the SMs; otherwise pairs, which
 // read each key tile half as often.  32768 tokens of 32/8 heads in prompts of 32, 64,
-// 96, 128, 192, 256 tokens take 130, 125, 123, 120, 164, 169 us one tile a CTA and 221,
-// 128, 148, 116, 142, 146 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
-// 80, 104, 128 tiles) 7.2, 9.3, 11.1, 13.0, 13.2 and 8.4, 10.5, 11.9, 12.6, 13.9; of
-// 16384 1927 and 1349.
+// 96, 128, 192, 256 tokens take 126, 120, 118, 117, 159, 166 us one tile a CTA and 204,
+// 119, 140, 109, 136, 142 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
+// 80, 104, 128 tiles) 7.2, 9.3, 11.0, 12.9, 13.1 and 8.0, 10.1, 11.9, 12.1, 13.8; of
+// 16384 1944 and 1352.
 template <int DQ, int DV>
 cudaError_t launch_prompt_d(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             const PromptParams& p, int num_sms, cudaStream_t stream) {
