@@ -9,9 +9,9 @@
 //
 // Bound by HBM: every cached key and value is read once and used for the G
 // query heads of its kv head only.  Measured on a GB300 (copy bandwidth 6.78 TB/s):
-// 256 sequences of 1024 to 32768 tokens, 8 kv heads of 128, 16.6 GB in 2.35 ms
-// (7.05 TB/s); 200 over an E4M3 cache 6.8 TB/s; one of 131071 tokens, 537 MB, in
-// 84 us (6.4 TB/s).  One of 1000 tokens takes 6.3 us, the latency of two launches
+// 256 sequences of 1024 to 32768 tokens, 8 kv heads of 128, 16.6 GB in 2.26 to 2.36 ms
+// (7.05 to 7.35 TB/s by box); 200 over an E4M3 cache 6.8 TB/s; one of 131071 tokens, 537 MB, in
+// 84 us (6.4 TB/s).  One of 1000 tokens takes 6.2 us, the latency of two launches
 // and of lengths -> block table -> page -> softmax -> join.
 //
 // Work split.  The pages (64-token blocks) of all sequences, in order, form
@@ -180,10 +180,16 @@ struct SeqWalk {
     const int i = from + (threadIdx.x & 31);
     mine = i < p.batch ? valid_ctx(p, __ldg(p.ctx + i)) : 0;
   }
-  __device__ __forceinline__ void start(const PagedDecodeParams& p, int at) {
-    load(p, at);
+  // From sequence `at` on; `few` are the lengths of the first 32 where there are no more.
+  __device__ __forceinline__ void start(const PagedDecodeParams& p, int at, int few) {
+    if (p.batch <= 32) {
+      base = 0;
+      mine = few;
+    } else {
+      load(p, at);
+    }
     b = at;
-    ctx = __shfl_sync(0xffffffffu, mine, 0);
+    ctx = __shfl_sync(0xffffffffu, mine, at - base);
   }
   // Goes on to the next non-empty sequence (there is one).
   __device__ __forceinline__ void next(const PagedDecodeParams& p) {
@@ -223,27 +229,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
 
   if (cols > 1) grid_launch_next();  // the join kernel may be placed beside this one
 
-  if (threadIdx.x == 0) {
-    *abort_flag = 0u;
-    for (int i = 0; i < C::NST; ++i) {
-      mbar_init(smem_u32(&bars[i]), 1);
-      mbar_init(smem_u32(&bars[C::NST + i]), kConsumers);
-    }
+  if (threadIdx.x == 0) *abort_flag = 0u;
+  if (threadIdx.x < 2 * C::NST) {
+    mbar_init(smem_u32(&bars[threadIdx.x]), threadIdx.x < C::NST ? 1 : kConsumers);
     fence_mbar_init();
   }
+  if (warp == kConsumers && lane < 4)
+    tma_prefetch_desc(lane == 0 ? &tm_k : lane == 1 ? &tm_v : lane == 2 ? &tm_k16 : &tm_v16);
   grid_wait();
   // ---- this column's pages
   int total, nc, first, last, start_b = 0, start_page = 0;  // start_page: pages of start_b before this column
+  int few = 0;  // this lane's length, where there are up to 32
   auto share_out = [&]() {
     nc = min(cols, total);  // columns with pages: at least one page each
     first = col < nc ? first_page(col, total, nc) : 0;
     last = col < nc ? first_page(col + 1, total, nc) : 0;  // one past
   };
-  auto pages_at = [&](int b, int end) {  // (an invalid length counts as 0 and is recorded once)
+  auto length_at = [&](int b, int end) {  // (an invalid length counts as 0 and is recorded)
     if (b >= end) return 0;
     const int raw = __ldg(p.ctx + b), c = valid_ctx(p, raw);
     if (c != raw && blockIdx.x == 0) record_status(p.status, kStatusInvalid);
-    return pages_of(c);
+    return c;
   };
   // Looks for the page `first` in the lanes' sequences, from `from` on, with `at` pages
   // before them.
@@ -265,7 +271,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
   };
   if (p.batch <= 32) {
     // every warp finds it by itself (one row of 1000 keys 6.8 -> 6.3 us)
-    const int n = pages_at(lane, p.batch), inc = prefix(n);
+    few = length_at(lane, p.batch);
+    const int n = pages_of(few), inc = prefix(n);
     total = __shfl_sync(0xffffffffu, inc, 31);
     share_out();
     if (first < last) locate(0, n, inc, 0);
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
     const int per = (p.batch + 4) / 5;
     const int b0 = min(p.batch, warp * per), b1 = min(p.batch, b0 + per);
     int sum = 0;
-    for (int b = b0; b < b1; b += 32) sum += pages_at(b + lane, b1);
+    for (int b = b0; b < b1; b += 32) sum += pages_of(length_at(b + lane, b1));
     sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) scan[warp] = sum;
     __syncthreads();
@@ -312,26 +319,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
 
   if (warp == kConsumers) {
     // ------------------------------------------------------ producer
-    if (h == 0 && lane == 0) {
-      // File the sequence that column col - 1 ends with and this one goes on
-      // with, if it began there: the parts of one sequence are one entry.
-      JoinDesc d{-1, 0, 0, 0};
-      if (n_pages > 0 && start_page > 0) {
-        const int begin = first - start_page;  // the sequence's first page
-        const int prev = first_page(col - 1, total, nc);
-        if (begin >= prev) {
-          const int64_t end = begin + pages_of(valid_ctx(p, __ldg(p.ctx + start_b)));  // one past
-          const int last_col = static_cast<int>((end * nc - 1) / total);
-          d = JoinDesc{start_b, last_col - col + 2, begin == prev ? 0 : 1, 0};
-        }
-      }
-      if (cols > 1) ws.desc[col] = d;
-    }
     if (n_pages > 0) {
-      if (lane == 0) {
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
-      }
+      // The first 32 entries of the block table load while the sequence's length does.
+      const int32_t* row = p.block_table + static_cast<int64_t>(start_b) * p.max_blocks_per_seq + start_page;
+      int32_t next_blk = lane < p.max_blocks_per_seq - start_page ? __ldg(row + lane) : 0;
       // Starts the copies of a page with `rest` tokens of its sequence left.
       auto copy_page = [&](int slot, int32_t blk, int rest) {
         const uint32_t full = smem_u32(&bars[slot]);
@@ -358,15 +349,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
         }
       };
       SeqWalk sw;
-      sw.start(p, start_b);
+      sw.start(p, start_b, few);
       int page = start_page, left = n_pages;
       int slot = 0;
       uint32_t phase = 0u, filled = 0u, fill_phase = 0u;
       bool ok = true;
       while (ok && left > 0) {
         const int np = min(pages_of(sw.ctx) - page, left);
-        const int32_t* row = p.block_table + static_cast<int64_t>(sw.b) * p.max_blocks_per_seq + page;
-        int32_t next_blk = lane < np ? __ldg(row + lane) : 0;
         for (int i = 0; ok && i < np; i += 32) {
           const int32_t blks = next_blk;  // lane l: block of page i + l
           // the next 32 entries load while these pages are copied
@@ -394,7 +383,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
         }
         left -= np;
         page = 0;
-        if (left > 0) sw.next(p);
+        if (left > 0) {
+          sw.next(p);
+          row = p.block_table + static_cast<int64_t>(sw.b) * p.max_blocks_per_seq;
+          next_blk = lane < min(pages_of(sw.ctx), left) ? __ldg(row + lane) : 0;
+        }
       }
       if (!ok && lane == 0) {
         // Let every copy land before the CTA exits.
@@ -402,13 +395,28 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
           if (filled & (1u << i)) mbar_wait_for(smem_u32(&bars[i]), (fill_phase >> i) & 1u, 100000000ull);
       }
     }
+    if (h == 0 && lane == 0) {
+      // File the sequence that column col - 1 ends with and this one goes on
+      // with, if it began there: the parts of one sequence are one entry.
+      JoinDesc d{-1, 0, 0, 0};
+      if (n_pages > 0 && start_page > 0) {
+        const int begin = first - start_page;  // the sequence's first page
+        const int prev = first_page(col - 1, total, nc);
+        if (begin >= prev) {
+          const int64_t end = begin + pages_of(valid_ctx(p, __ldg(p.ctx + start_b)));  // one past
+          const int last_col = static_cast<int>((end * nc - 1) / total);
+          d = JoinDesc{start_b, last_col - col + 2, begin == prev ? 0 : 1, 0};
+        }
+      }
+      if (cols > 1) ws.desc[col] = d;
+    }
     return;
   }
 
   // -------------------------------------------------------- consumers
   // Rows of length 0: zeros, and -inf for the log of an empty sum.
   for (int b = col; b < p.batch; b += cols) {
-    if (valid_ctx(p, __ldg(p.ctx + b)) > 0) continue;
+    if ((p.batch <= 32 ? __shfl_sync(0xffffffffu, few, b) : valid_ctx(p, __ldg(p.ctx + b))) > 0) continue;
     uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * p.heads + h * G) * DV);
     for (int i = threadIdx.x; i < G * DV / 8; i += 32 * kConsumers) dst[i] = make_uint4(0u, 0u, 0u, 0u);
     if (p.lse && threadIdx.x < G) p.lse[static_cast<int64_t>(h * G + threadIdx.x) * p.batch + b] = -INFINITY;
@@ -426,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
   const int vrow = F8 ? krow : warp * 16 + (mi >> 1) * 8 + r8, vchunk = F8 ? kchunk : mi & 1;
 
   SeqWalk sw;
-  sw.start(p, start_b);
+  sw.start(p, start_b, few);
   int page = start_page, left = n_pages;
   int slot = 0;
   uint32_t phase = 0u;
