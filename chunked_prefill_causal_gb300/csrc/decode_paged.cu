@@ -9,10 +9,11 @@
 //
 // Bound by HBM: every cached key and value is read once and used for the G
 // query heads of its kv head only.  Measured on a GB300 (copy bandwidth 6.78 TB/s):
-// 256 sequences of 1024 to 32768 tokens, 8 kv heads of 128, 16.6 GB in 2.26 to 2.36 ms
-// (7.05 to 7.35 TB/s by box); 200 over an E4M3 cache 6.8 TB/s; one of 131071 tokens, 537 MB, in
-// 84 us (6.4 TB/s).  One of 1000 tokens takes 6.2 us, the latency of two launches
-// and of lengths -> block table -> page -> softmax -> join.
+// 256 sequences of 1024 to 32768 tokens, 8 kv heads of 128, 16.6 GB in 2.26 to
+// 2.36 ms (7.05 to 7.35 TB/s by machine); 200 over an E4M3 cache 6.8 TB/s; one of
+// 131071 tokens, 537 MB, in 82 to 84 us (6.4 to 6.5 TB/s).  One of 1000 tokens takes
+// 6.2 us, the latency of two launches and of lengths -> block table -> page -> softmax
+// -> join.
 //
 // Work split.  The pages (64-token blocks) of all sequences, in order, form
 // one list of N pages.  It is cut into `cols` equal parts whatever the
@@ -728,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
           else
             *reinterpret_cast<uint2*>(out) = make_uint2(pk[0], pk[1]);
           if (p.lse && d0 == 0)
-            p.lse[static_cast<int64_t>(hq) * p.batch + sw.b] = den > 0.f ? top * kLn2p + logf(den) : (den == den ? -INFINITY : den);
+            p.lse[static_cast<int64_t>(hq) * p.batch + sw.b] =
+                den > 0.f ? top * kLn2p + logf(den) : (den == den ? -INFINITY : den);
         } else {
           const int64_t at = static_cast<int64_t>(part) * p.heads + hq;
 #pragma unroll

@@ -825,9 +825,10 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
         tmem_ld_wait();
         uint32_t w[4][4];  // [piece of 8 dims][word]
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-        {
-          const float2 e = ffma2(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])), make_float2(inv, inv), make_float2(-0.f, -0.f));
+        for (int k = 0; k < 16; ++k) {
+          // (two products an instruction; -0 as the addend leaves them as they are)
+          const float2 e = ffma2(make_float2(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1])),
+                                 make_float2(inv, inv), make_float2(-0.f, -0.f));
           w[k >> 2][k & 3] = pack_bf16x2(e.x, e.y);
         }
         transpose4(w, a);
