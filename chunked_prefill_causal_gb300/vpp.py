@@ -131,6 +131,24 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, like, stream):
+    """Memory for a kernel on `stream` (the current one when None) to write, from that stream's pool: work queued on the
+    current stream, which `stream` does not wait for, may still use what its own pool hands out."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _output(shape, dtype, like, stream):
+    """_empty for what the caller gets: freed, it is not written again before the work that the caller's current stream has
+    queued by then has read it."""
+    t = _empty(shape, dtype, like, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
@@ -191,7 +209,7 @@ def vpp_chunk_attn(q, k_cache, v_cache, prefix_len, out=None, lse=None, stream=N
     C, H, d = q.shape
     Hkv = k_cache.shape[1]
     if out is None:
-        out = torch.empty((C, H, d), dtype=torch.bfloat16, device=q.device)
+        out = _output((C, H, d), torch.bfloat16, q, stream)
     _check("vpp_chunk_attn", load().vpp_chunk_attn(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), int(prefix_len), C, H, Hkv, d, _ptr(out), _ptr(lse),
         _stream(stream)))
@@ -231,10 +249,10 @@ def vpp_chunk_attn_ex(q, k_cache, v_cache, prefix_len, block_table=None, out=Non
     else:
         nb = k_cache.shape[0]  # contiguous: capacity in tokens
     if out is None:
-        out = torch.empty((C, H, dv), dtype=torch.bfloat16, device=q.device)
+        out = _output((C, H, dv), torch.bfloat16, q, stream)
     need = chunk_attn_workspace_size(qd, prefix_len, C, H, Hkv, dq, dv, num_splits)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("vpp_chunk_attn_ex", load().vpp_chunk_attn_ex(
         _ptr(q), qd, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), nb, int(prefix_len), C, H, Hkv,
@@ -255,7 +273,7 @@ def vpp_chunk_attn_noalloc(q, k_cache, v_cache, prefix_len, block_table=None, ou
     if q.dtype != torch.bfloat16:
         raise ValueError("vpp_chunk_attn_noalloc takes bf16 q")
     if out is None:
-        out = torch.empty((C, H, dv), dtype=torch.bfloat16, device=q.device)
+        out = _output((C, H, dv), torch.bfloat16, q, stream)
     _check("vpp_chunk_attn_noalloc", load().vpp_chunk_attn_noalloc(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), k_cache.shape[0], int(prefix_len), C, H,
         Hkv, dq, dv, float(softmax_scale), int(num_splits), _ptr(out), _ptr(lse), _stream(stream)))
@@ -279,10 +297,10 @@ def vpp_mixed_attn(q, k_cache, v_cache, block_table, cu_seqlens_q, ctx_lens, out
     cu, cu_p = _i32_host(cu_seqlens_q)
     ctx, ctx_p = _i32_host(ctx_lens)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=torch.bfloat16, device=q.device)
+        out = _output((T, H, dv), torch.bfloat16, q, stream)
     need = mixed_attn_workspace_size(cu, ctx, H, Hkv, dq, dv)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("vpp_mixed_attn", load().vpp_mixed_attn(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1],
@@ -360,11 +378,11 @@ def vpp_chunk_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_len, block_
     dv = v_cache.shape[-1]
     _scales(k_scale, v_scale, Hkv)
     if out is None:
-        out = torch.empty((C, H, dv), dtype=torch.bfloat16, device=q.device)
+        out = _output((C, H, dv), torch.bfloat16, q, stream)
     if workspace is None:
         size = chunk_attn_fp8_widen_workspace_size if widen else chunk_attn_fp8_workspace_size
         need = size(prefix_len, C, H, Hkv, dq, dv, num_splits)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 256), torch.uint8, q, stream)
     wbytes = workspace.numel() * workspace.element_size()
     _check("vpp_chunk_attn_fp8", load().vpp_chunk_attn_fp8(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
@@ -398,10 +416,10 @@ def vpp_mixed_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_se
     cu, cu_p = _i32_host(cu_seqlens_q)
     ctx, ctx_p = _i32_host(ctx_lens)
     if out is None:
-        out = torch.empty((T, H, dv), dtype=torch.bfloat16, device=q.device)
+        out = _output((T, H, dv), torch.bfloat16, q, stream)
     need = (mixed_attn_fp8_widen_workspace_size if widen else mixed_attn_fp8_workspace_size)(cu, ctx, H, Hkv, dq, dv)
     if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(need, torch.uint8, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check("vpp_mixed_attn_fp8", load().vpp_mixed_attn_fp8(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
@@ -415,7 +433,7 @@ def topk_chunk_attn_workspace_size(chunk_len, topk, heads, head_dim):
     return int(load().vpp_topk_chunk_attn_workspace_size(int(chunk_len), int(topk), heads, head_dim))
 
 
-def _topk_args(q, k_cache, topk_idx, topk_len, workspace):
+def _topk_args(q, k_cache, topk_idx, topk_len, workspace, stream):
     if topk_idx.dtype != torch.int32 or topk_len.dtype != torch.int32:
         raise ValueError("topk_idx and topk_len are int32")
     C, H, d = q.shape
@@ -425,7 +443,7 @@ def _topk_args(q, k_cache, topk_idx, topk_len, workspace):
     if workspace is None:
         need = topk_chunk_attn_workspace_size(C, topk, H, d)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = _empty(need, torch.uint8, q, stream)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return C, H, d, topk, workspace, wbytes
 
@@ -435,10 +453,10 @@ def vpp_topk_chunk_attn(q, k_cache, v_cache, prefix_len, topk_idx, topk_len, blo
     """Top-k sparse prefix attention of a chunk (bf16 q and cache): query token i
     attends the key positions topk_idx[i, :topk_len[i]] (int32 CUDA tensors)."""
     _need_cuda(q, k_cache, v_cache, topk_idx, topk_len, block_table, out, lse, workspace)
-    C, H, d, topk, workspace, wbytes = _topk_args(q, k_cache, topk_idx, topk_len, workspace)
+    C, H, d, topk, workspace, wbytes = _topk_args(q, k_cache, topk_idx, topk_len, workspace, stream)
     Hkv = k_cache.shape[-2]
     if out is None:
-        out = torch.empty((C, H, d), dtype=torch.bfloat16, device=q.device)
+        out = _output((C, H, d), torch.bfloat16, q, stream)
     _check("vpp_topk_chunk_attn", load().vpp_topk_chunk_attn(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), k_cache.shape[0], int(prefix_len), C,
         _ptr(topk_idx), _ptr(topk_len), topk, H, Hkv, d, float(softmax_scale), _ptr(out), _ptr(lse),
@@ -451,11 +469,11 @@ def vpp_topk_chunk_attn_fp8(q, k_cache, v_cache, k_scale, v_scale, prefix_len, t
     """vpp_topk_chunk_attn over an E4M3 cache (uint8 codes, per-kv-head scales)."""
     _need_cuda(q, k_cache, v_cache, topk_idx, topk_len, block_table, out, lse, workspace)
     _fp8_cache(k_cache, v_cache)
-    C, H, d, topk, workspace, wbytes = _topk_args(q, k_cache, topk_idx, topk_len, workspace)
+    C, H, d, topk, workspace, wbytes = _topk_args(q, k_cache, topk_idx, topk_len, workspace, stream)
     Hkv = k_cache.shape[-2]
     _scales(k_scale, v_scale, Hkv)
     if out is None:
-        out = torch.empty((C, H, d), dtype=torch.bfloat16, device=q.device)
+        out = _output((C, H, d), torch.bfloat16, q, stream)
     _check("vpp_topk_chunk_attn_fp8", load().vpp_topk_chunk_attn_fp8(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), k_cache.shape[0],
         int(prefix_len), C, _ptr(topk_idx), _ptr(topk_len), topk, H, Hkv, d, float(softmax_scale), _ptr(out),
@@ -494,18 +512,10 @@ def _stream_ptr(stream, dev):
     return _raw_stream(dev) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
-def _empty(shape, dtype, like, stream):
-    """A tensor for a kernel on `stream` (the current one when None) to write."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _rope_append(name, q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_q, ctx_lens, q_out, k_out,
                  rot_start, interleaved, stream):
     if q is not None and q_out is None:
-        q_out = _empty(q.shape, torch.bfloat16, q, stream)
+        q_out = _output(q.shape, torch.bfloat16, q, stream)
     dev = torch.cuda.current_device()
     code = _calls().rope(dev, _stream_ptr(stream, dev), q, k, v, cos_sin, k_cache, v_cache, k_scale, v_scale, block_table,
                          cu_seqlens_q, ctx_lens, q_out, k_out, rot_start, interleaved)
@@ -555,7 +565,7 @@ def _decode_attn(name, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_l
     dev = torch.cuda.current_device()
     raw = _stream_ptr(stream, dev)
     if out is None:
-        out = _empty((q.shape[0], q.shape[1], v_cache.shape[3]), torch.bfloat16, q, stream)
+        out = _output((q.shape[0], q.shape[1], v_cache.shape[3]), torch.bfloat16, q, stream)
     own = None
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -587,7 +597,8 @@ def vpp_decode_attn(q, k_cache, v_cache, block_table, ctx_lens, out=None, lse=No
     bf16 paged cache; ctx_lens (int32 CUDA tensor) is read when the kernel
     runs, and a row of length 0 gives out = 0, lse = -inf.  Without a
     workspace the calls of a thread on the current stream share one; calls
-    under capture or on a given stream allocate their own."""
+    under capture or on a given stream allocate their own, from the memory of
+    the stream that they run on."""
     return _decode_attn("vpp_decode_attn", q, k_cache, v_cache, None, None, block_table, ctx_lens, out, lse, softmax_scale,
                         workspace, stream)
 
@@ -606,7 +617,7 @@ def vpp_prompt_attn(q, k, v, cu_seqlens, out=None, lse=None, softmax_scale=0.0, 
     bf16 [tokens, heads, d], contiguous or parts of one fused projection);
     cu_seqlens (int32 CUDA tensor) is read when the kernel runs."""
     if out is None:
-        out = _empty((q.shape[0], q.shape[1], v.shape[2]), torch.bfloat16, q, stream)
+        out = _output((q.shape[0], q.shape[1], v.shape[2]), torch.bfloat16, q, stream)
     dev = torch.cuda.current_device()
     code = _calls().prompt(dev, _stream_ptr(stream, dev), q, k, v, cu_seqlens, out, lse, softmax_scale)
     if code != VPP_OK:
