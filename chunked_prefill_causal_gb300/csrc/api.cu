@@ -1165,6 +1165,8 @@ bool strided_ok(const void* p, int64_t stride, int64_t row) {
 }
 
 constexpr int64_t kMaxPackedRows = INT32_MAX / 2;
+// Sequences of a call: sums of two indexes, and steps past the last one, fit 32 bits.
+constexpr int32_t kMaxSequences = INT32_MAX / 2;
 
 // Packed q: a box is 64 dims x G heads x 1 kv head x floor(128 / G) tokens.
 int make_packed_q_map(CUtensorMap* m, const void* q, int64_t stride, int64_t total_q, int heads, int kv_heads, int dq) {
@@ -1184,7 +1186,7 @@ int make_packed_kv_map(CUtensorMap* m, const void* x, int64_t stride, int64_t to
 }
 
 int rope_append_impl(bool fp8, RopeParams p, int interleaved, cudaStream_t st) {
-  if (p.total_q < 0 || p.total_q > kMaxPackedRows || p.batch < 0) return VPP_ERR_INVALID;
+  if (p.total_q < 0 || p.total_q > kMaxPackedRows || p.batch < 0 || p.batch > kMaxSequences) return VPP_ERR_INVALID;
   if (p.total_q == 0) return VPP_OK;  // pointers may be NULL without rows
   if (p.batch == 0 || !p.cu || !aligned4(p.cu) || !aligned4(p.ctx)) return VPP_ERR_INVALID;
   if (p.kv_heads <= 0 || p.kv_heads > 1024 || (p.q && (p.heads <= 0 || p.heads > 16384))) return VPP_ERR_INVALID;
@@ -1233,7 +1235,7 @@ int make_decode_map(CUtensorMap* m, const void* cache, int32_t num_blocks, int k
 
 int decode_attn_impl(bool fp8, PagedDecodeParams p, float softmax_scale, void* workspace, size_t workspace_bytes,
                      cudaStream_t st) {
-  if (p.batch < 0) return VPP_ERR_INVALID;
+  if (p.batch < 0 || p.batch > kMaxSequences) return VPP_ERR_INVALID;
   if (p.batch == 0) return VPP_OK;  // pointers may be NULL without rows
   if (int r = check_groups(p.heads, p.kv_heads)) return r;
   if (!supported_dims(p.dq, p.dv) || p.kv_heads > 1024) return VPP_ERR_UNSUPPORTED;
@@ -1318,7 +1320,7 @@ int vpp_decode_attn_fp8(const void* q, int64_t q_stride, const void* k_cache, co
 }
 
 size_t vpp_decode_attn_workspace_size(int32_t batch, int heads, int kv_heads, int head_dim_qk, int head_dim_v) {
-  if (batch <= 0 || check_groups(heads, kv_heads) || !supported_dims(head_dim_qk, head_dim_v) || kv_heads > 1024)
+  if (batch <= 0 || batch > kMaxSequences || check_groups(heads, kv_heads) || !supported_dims(head_dim_qk, head_dim_v) || kv_heads > 1024)
     return 0;
   DeviceState* ds = nullptr;
   const int num_sms = device_state(&ds) == VPP_OK ? ds->num_sms : 152;
@@ -1329,7 +1331,7 @@ int vpp_prompt_attn(const void* q, int64_t q_stride, const void* k, int64_t k_st
                     int64_t v_stride, const int32_t* cu_seqlens, int32_t batch, int64_t total_q, int heads,
                     int kv_heads, int head_dim_qk, int head_dim_v, float softmax_scale, void* out, float* lse,
                     void* stream) {
-  if (total_q < 0 || total_q > kMaxPackedRows || batch < 0) return VPP_ERR_INVALID;
+  if (total_q < 0 || total_q > kMaxPackedRows || batch < 0 || batch > kMaxSequences) return VPP_ERR_INVALID;
   if (total_q == 0) return VPP_OK;  // pointers may be NULL without rows
   if (batch == 0 || !cu_seqlens || !aligned4(cu_seqlens)) return VPP_ERR_INVALID;
   if (int r = check_groups(heads, kv_heads)) return r;

@@ -423,7 +423,8 @@ size_t vpp_topk_chunk_attn_workspace_size(int64_t chunk_len, int32_t topk,
  * q, k and v are given with their token stride in elements (a multiple of 8,
  * at least heads x d), so they may be parts of one fused projection
  * [total_q][heads dq + kv_heads dq + kv_heads dv]; out, lse and the caches
- * are contiguous.  heads / kv_heads is any whole number from 1 to 16.
+ * are contiguous.  heads / kv_heads is any whole number from 1 to 16; batch
+ * and total_q are below 2^30.
  */
 
 /*
