@@ -23,7 +23,7 @@
 // same number of pages.  The CTAs of one column are neighbours in launch order and
 // read the same blocks at the same time, head by head.  A sequence
 // inside one column is finished there; one that crosses columns leaves a
-// float32 partial (sum, max, denominator) per column, which decode_join_kernel adds up
+// float32 partial (sum, reference, denominator) per column, which decode_join_kernel adds up
 // ("02 · 并行策略与 PP 切分" note, §7).  A column has at most two such
 // sequences, its first and its last.
 //
@@ -62,6 +62,19 @@ namespace {
 constexpr float kLn2p = 0.69314718055994530942f;
 constexpr int kConsumers = 4;
 constexpr int kThreads = 32 * (kConsumers + 1);
+
+// A weight is 2^(score - m) for a reference m that is 2^kLift below the running maximum
+// when it is taken and moves when the maximum has grown by more than 2^kGrow since (exact
+// either way: numerator and denominator share it).  Over an E4M3 cache the weights
+// become f16 operands, whose largest value is below 2^16: the largest weight lies in
+// 2^14 .. 2^15, so a weight is rounded relatively (2^-11) down to 2^-28 of the largest one
+// and absolutely (2^-39 of it) below.  (With the maximum itself as the reference, keys of
+// 2^-25 of it and less were lost to the numerator, not to the denominator.)  bf16 operands
+// have float32's range.
+template <bool F8>
+constexpr float kLift = F8 ? 14.0f : 0.0f;
+template <bool F8>
+constexpr float kGrow = F8 ? 1.0f : 8.0f;
 
 // CTAs per SM: three where a stage is small and the registers of q and O leave room in
 // 128, else two.  (Two groups of heads over an E4M3 cache, 1.2 GB, two and three CTAs:
@@ -151,8 +164,8 @@ struct JoinDesc {
 };
 
 struct Workspace {
-  float* o;      // [cols][2][heads][dv], sums relative to 2^max
-  float2* ml;    // [cols][2][heads], (max, denominator)
+  float* o;      // [cols][2][heads][dv], sums relative to 2^reference
+  float2* ml;    // [cols][2][heads], (reference, denominator)
   JoinDesc* desc;  // [cols]
 };
 
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
     const int seq_pages = pages_of(sw.ctx);
     const int np = min(seq_pages - page, left);
     if (F8) scale_q();
-    float m[NG][2], l[NG][2];  // running maxima, and this lane's part of the denominators
+    float m[NG][2], l[NG][2];  // references of the weights, and this lane's part of the denominators
     float o[NG][C::NT][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
@@ -551,8 +564,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
           sc[e] = (s[n][0][e] + s[n][1][e]) * rs[n][e & 1];
           if (TAIL && g + 8 * (e >> 1) >= live) sc[e] = -INFINITY;
         }
-        // ---- online softmax of the two heads (eight lanes hold a head); the
-        // reference moves only when the maximum has grown by more than 2^8
+        // ---- online softmax of the two heads (eight lanes hold a head)
         float f[2];
         bool moved = false;
 #pragma unroll
@@ -562,9 +574,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
           f[c] = 1.f;
-          if (mx > m[n][c] + 8.0f || (m[n][c] == -INFINITY && mx > -INFINITY)) {
-            f[c] = ex2_approx(m[n][c] - mx);
-            m[n][c] = mx;
+          if (mx > m[n][c] + (kLift<F8> + kGrow<F8>) || (m[n][c] == -INFINITY && mx > -INFINITY)) {
+            const float to = mx - kLift<F8>;
+            f[c] = ex2_approx(m[n][c] - to);
+            m[n][c] = to;
             moved = true;
           }
         }
@@ -588,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
           l[n][c] += pv[c] + pv[2 + c];
         }
         // P is rounded to the operand type of V (bf16, relative 2^-8; f16 over an
-        // E4M3 cache, 2^-11); the denominator keeps float32.
+        // E4M3 cache, see kLift); the denominator keeps float32.
         // Its accumulator fragment, transposed, is the operand's.
         pb[n][0] = transpose8x8(F8 ? pack_half2(pv[0], pv[1]) : pack_bf16x2(pv[0], pv[1]));
         pb[n][1] = transpose8x8(F8 ? pack_half2(pv[2], pv[3]) : pack_bf16x2(pv[2], pv[3]));
