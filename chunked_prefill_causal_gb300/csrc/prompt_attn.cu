@@ -803,7 +803,8 @@ __global__ void __launch_bounds__(PShape<DQ, DV, PAIR>::THREADS, PShape<DQ, DV, 
       // these loads.
       const bool valid = tok < it.len && row < G * T;
       const int hq = it.g * G + row_head;
-      const float inv = 1.f / l;
+      // (a row whose scores are all -inf: 0)
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       // A thread holds a row, whose direct 16-byte stores would touch 32 lines
       // an instruction (3 us an item).  Each 32 dims are transposed within groups of four lanes
       // first: lane a of a group gets dims 8a .. 8a + 7 of the group's four

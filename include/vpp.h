@@ -501,9 +501,10 @@ int vpp_rope_append_fp8(const void *q, int64_t q_stride, const void *k,
  * [batch][max_blocks_per_seq]); ctx_lens[b] counts the row's own token, which
  * must already be in the cache.  A row with ctx_lens[b] == 0 (padding) gets
  * out = 0 and lse = -inf, and so does one whose length is negative or longer
- * than its block-table row, which is recorded as VPP_ERR_INVALID.  A block
- * outside the pool reads as zeros and is recorded as VPP_ERR_INVALID.  Cache
- * rows past a sequence's length may hold anything.
+ * than its block-table row, which is recorded as VPP_ERR_INVALID, and a row
+ * whose scores are all -inf.  A block outside the pool reads as zeros and is
+ * recorded as VPP_ERR_INVALID.  Cache rows past a sequence's length may hold
+ * anything.
  * out [batch][heads][head_dim_v] bf16, lse [heads][batch] float32 (NULL
  * allowed).  head dims as in the conventions, kv_heads up to 1024,
  * batch x max_blocks_per_seq below 2^31.
@@ -551,6 +552,7 @@ size_t vpp_decode_attn_workspace_size(int32_t batch, int heads, int kv_heads,
  * earlier ones of its 128-token tile).  A sequence whose range is not within
  * 0 .. total_q or ends before it begins is left out and recorded as
  * VPP_ERR_INVALID.
+ * A row whose scores are all -inf gets out = 0 and lse = -inf.
  * out [total_q][heads][head_dim_v] bf16, lse [heads][total_q] float32 (NULL
  * allowed).  No workspace; total_q == 0 is a no-op.
  */
