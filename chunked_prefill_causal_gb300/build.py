@@ -1,6 +1,6 @@
 """Builds libvpp.so (sm_103a) in-tree: one nvcc -c per .cu file, in parallel,
-then one shared-library link with the CUDA runtime linked statically; and the
-binding's call module (csrc/pycall.cpp)."""
+then one shared-library link with the CUDA runtime linked statically; and, where
+torch is installed, the binding's call module (csrc/pycall.cpp)."""
 
 from __future__ import annotations
 
@@ -50,8 +50,13 @@ def call_module_path():
 
 def _call_module():
     """Compiles csrc/pycall.cpp, the argument marshalling of the serving-step calls (a CPython extension module that reads
-    torch tensors; host code only)."""
-    import torch
+    torch tensors; host code only).  Without a torch there is no binding to serve, and the library alone is built."""
+    try:
+        import torch
+    except ModuleNotFoundError as e:
+        if e.name != "torch":
+            raise
+        return
 
     src, so = os.path.join(CSRC, "pycall.cpp"), call_module_path()
     if _stale(so, src, os.path.getmtime(os.path.join(INCLUDE, "vpp.h"))):
