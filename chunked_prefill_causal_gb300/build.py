@@ -42,10 +42,10 @@ def _stale(obj, src, hdr_mtime):
 
 
 def call_module_path():
-    """The call module's file, which names the torch whose headers it was compiled with."""
+    """The call module's file, which names the torch and the Python whose headers it was compiled with."""
     import torch
 
-    return os.path.join(OUT_DIR, f"_vppcall-{torch.__version__}.so")
+    return os.path.join(OUT_DIR, f"_vppcall-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _call_module():

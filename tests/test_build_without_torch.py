@@ -40,3 +40,17 @@ def test_a_broken_torch_is_not_taken_for_a_missing_one():
             "            raise ImportError('broken', name=name)\nsys.meta_path.insert(0, Broken())\n"
             "from chunked_prefill_causal_gb300 import build\nbuild.build()")
     assert r.returncode != 0 and "broken" in r.stderr
+
+
+def test_the_call_module_names_its_python(monkeypatch):
+    """Its binary interface is that of one Python and one torch: another of either never loads it."""
+    import sysconfig
+
+    from chunked_prefill_causal_gb300 import build
+    mine = build.call_module_path()
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-some-os.so" if name == "EXT_SUFFIX" else None)
+    assert build.call_module_path() != mine
+    monkeypatch.undo()
+    import torch
+    monkeypatch.setattr(torch, "__version__", "0.0.0")
+    assert build.call_module_path() != mine
