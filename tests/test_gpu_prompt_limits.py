@@ -35,3 +35,75 @@ def test_rows_whose_scores_are_all_minus_infinity(H, Hkv, dq, dv, lens):
         lo, hi = int(cu[b]), int(cu[b]) + n
         ref = attend(q[lo:hi, G:], k[lo:hi, 1:], v[lo:hi, 1:], dq ** -0.5, True)
         check_attention(out[lo:hi, G:], lse[G:, lo:hi], ref, dq, HALF_BF16, f"sequence {b}")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("H,Hkv,dq,dv", [(32, 8, 128, 128), (24, 24, 192, 128), (12, 1, 192, 64), (5, 1, 64, 128), (8, 8, 64, 64), (26, 2, 128, 64)])
+def test_hostile_neighbours_of_long_sequences(H, Hkv, dq, dv, bad):
+    """Sequences of many key tiles with partial last ones, several items a CTA, hostile values before, between and behind them."""
+    lens = [40, 700, 1, 1500, 130, 300, 129, 385, 64, 1027, 5]
+    good = [1, 3, 5, 7, 9]
+    cu = starts(lens)
+    T = int(cu[-1]) + 77
+    q, k, v = randn((T, H, dq), 4), randn((T, Hkv, dq), 5), randn((T, Hkv, dv), 6)
+    live = torch.zeros(T, dtype=torch.bool)
+    for b in good:
+        live[int(cu[b]):int(cu[b + 1])] = True
+    for x in (q, k, v):
+        x[~live] = bad
+    lse = torch.empty((H, T), device=DEV)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    for b in good:
+        lo, hi = int(cu[b]), int(cu[b + 1])
+        ref = attend(q[lo:hi], k[lo:hi], v[lo:hi], dq ** -0.5, True)
+        check_attention(out[lo:hi], lse[:, lo:hi], ref, dq, HALF_BF16, f"sequence {b}")
+
+
+@pytest.mark.parametrize("H,Hkv,lens", [(1024, 1024, [3, 200]), (2048, 1024, [70, 1]), (1000, 500, [33, 129])])
+def test_many_kv_heads(H, Hkv, lens):
+    d = 64
+    cu = starts(lens)
+    T = int(cu[-1])
+    q, k, v = randn((T, H, d), 7), randn((T, Hkv, d), 8), randn((T, Hkv, d), 9)
+    lse = torch.empty((H, T), device=DEV)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    for b, n in enumerate(lens):
+        lo, hi = int(cu[b]), int(cu[b]) + n
+        ref = attend(q[lo:hi], k[lo:hi], v[lo:hi], d ** -0.5, True)
+        check_attention(out[lo:hi], lse[:, lo:hi], ref, d, HALF_BF16, f"sequence {b}")
+
+
+def test_a_hundred_thousand_sequences_mostly_empty():
+    H, Hkv, d = 4, 2, 64
+    lens = [0] * 100000
+    for i, n in ((0, 3), (127, 1), (128, 200), (50000, 17), (99999, 90)):
+        lens[i] = n
+    cu = starts(lens)
+    T = int(cu[-1])
+    q, k, v = randn((T, H, d), 10), randn((T, Hkv, d), 11), randn((T, Hkv, d), 12)
+    lse = torch.empty((H, T), device=DEV)
+    out = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV), lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    for lo, hi in sorted({(int(a), int(b)) for a, b in zip(cu, cu[1:]) if b > a}):
+        ref = attend(q[lo:hi], k[lo:hi], v[lo:hi], d ** -0.5, True)
+        check_attention(out[lo:hi], lse[:, lo:hi], ref, d, HALF_BF16, f"rows {lo} to {hi}")
+
+
+def test_the_cached_path_gives_the_same_attention():
+    """The packed call and the host-planned call over a paged cache: each is within its own distance of the formula, so they are
+    within both of each other."""
+    H, Hkv, d, n = 16, 4, 128, 700
+    q, k, v = (randn((n, h, d), 14 + h) for h in (H, Hkv, Hkv))
+    cu = torch.tensor([0, n], dtype=torch.int32)
+    table = torch.arange((n + 63) // 64, dtype=torch.int32, device=DEV)[None]
+    kc = torch.zeros((table.shape[1], 64, Hkv, d), dtype=torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    vpp.vpp_kv_append_varlen(k.to(DEV), v.to(DEV), kc, vc, table, cu.numpy(), [n])
+    a = vpp.vpp_mixed_attn(q.to(DEV), kc, vc, table, cu.numpy(), [n]).double().cpu()
+    b = vpp.vpp_prompt_attn(q.to(DEV), k.to(DEV), v.to(DEV), cu.to(DEV)).double().cpu()
+    o, _, absw, _ = attend(q, k, v, d ** -0.5, True)
+    # each side: P to bf16, one rounding of the result to bf16 (see check_attention; 2^-14 holds its float32 terms at these sizes)
+    tol = 2 * (HALF_BF16 * o.abs() + (HALF_BF16 + 2.0 ** -14) * absw)
+    assert bool(((a - b).abs() <= tol).all())
