@@ -493,7 +493,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(DQ, DV, F8, NG))
           amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(qb[n][s][i])), fabsf(bf16_hi(qb[n][s][i]))));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
       amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      const int e = (amax > 0.f && amax < INFINITY) ? max(-60, min(60, 14 - ilogbf(amax))) : 0;
+      // (-113 at least; 126 at most, so that 2^e is a float32: reached below 2^-112)
+      const int e = (amax > 0.f && amax < INFINITY) ? min(126, 14 - ilogbf(amax)) : 0;
       const float up = ldexpf(1.f, e), down = sl * ldexpf(1.f, -e);
       rs[n][0] = __shfl_sync(0xffffffffu, down, 8 * u);  // lane 4 (2u) holds head 2u
       rs[n][1] = __shfl_sync(0xffffffffu, down, 8 * u + 4);

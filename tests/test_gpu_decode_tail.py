@@ -45,3 +45,23 @@ def test_a_tail_below_a_dominant_key_keeps_its_weight(H, Hkv, n, depth, at):
     worst = float(((out.double().cpu() - o).abs() / tol).max())
     assert worst <= 1.0, f"off by {worst:.3f} of the tolerance"
     assert float((lse.double().cpu() - l).abs().max()) <= 2.0 ** -16 + 2.0 ** -22 * float(l.abs().max())
+
+
+@pytest.mark.parametrize("power", [120, 100, 76, 75, 60, 0, -40, -60, -90, -110])
+@pytest.mark.parametrize("H,Hkv,d", [(8, 2, 128), (12, 1, 64)])
+def test_queries_of_any_size(H, Hkv, d, power):
+    """Queries scaled by a power of two and a softmax scale that takes it back give the rows of the unscaled ones: they are
+    exact multiples in bf16, and the scores differ by nothing."""
+    g = torch.Generator().manual_seed(1)
+    n = 300
+    kc, vc = (torch.randn((5, 64, Hkv, d), generator=g).to(torch.float8_e4m3fn).view(torch.uint8).to(DEV) for _ in range(2))
+    q = torch.randn((2, H, d), generator=g).to(torch.bfloat16).double()
+    one = torch.ones(Hkv, device=DEV)
+    table = torch.arange(5, dtype=torch.int32, device=DEV).expand(2, 5).contiguous()
+    ctx = torch.tensor([n, 17], dtype=torch.int32, device=DEV)
+    got = []
+    for e in (0, power):
+        lse = torch.empty((H, 2), device=DEV)
+        out = vpp.vpp_decode_attn_fp8((q * 2.0 ** e).to(torch.bfloat16).to(DEV), kc, vc, one, one, table, ctx, lse=lse, softmax_scale=0.125 * 2.0 ** -e)
+        got.append((out.cpu(), lse.cpu()))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
