@@ -898,20 +898,37 @@ cudaError_t launch_prompt_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, co
                            tm_q, tm_k, tm_v, p);
 }
 
-// One query tile a CTA, two CTAs per SM, where sequences have up to one key tile on
-// average, or the tiles occupy up to three fifths of the SMs; otherwise pairs, which
-// read each key tile half as often.  32768 tokens of 32/8 heads in prompts of 32, 64,
-// 96, 128, 192, 256 tokens take 126, 120, 118, 117, 159, 166 us one tile a CTA and 204,
-// 119, 140, 109, 136, 142 in pairs; one prompt of 77, 200, 300, 400, 500 tokens (24, 56,
-// 80, 104, 128 tiles) 7.2, 9.3, 11.0, 12.9, 13.1 and 8.0, 10.1, 11.9, 12.1, 13.8; of
-// 16384 1944 and 1352.
+// One query tile a CTA, two CTAs per SM, for short sequences and for few tiles; otherwise
+// pairs, which read each key tile half as often but run a tile that has no partner alone.
+// The host knows the rows and the number of sequences, not the lengths.
+//
+// Short: up to 96 rows a sequence, or as many as a tile holds (groups of 1), or 128 at
+// 64/64 dims.  One tile a CTA and pairs, us, about 32768 tokens in equal prompts:
+//   tokens a prompt          48        64        96       112       128
+//   32/8 heads of 128   145 146   119 119   118 139   131 124   117 107
+//   16/8                 78 135    67 105    77  77    70  69    63  63
+//   64/8                228 271   225 219   224 217   226 237   224 204
+//   32/8 heads of 64    107 125    85  97    85 117    98 104    86  89
+//   8/8 heads of 128                58 101    46  70              45  54
+// and 300 prompts of random lengths, means 64, 96 and 128: 32/8 heads of 128 87 95,
+// 143 140, 189 177; 64/8 150 154, 255 238, 341 306; 32/8 of 64 64 80, 101 119, 130 151.
+// (96 loses up to 7% for random lengths, less would lose 18% for equal ones.)
+// Lengths that are far apart are misjudged, and so are empty sequences and rows of no
+// sequence: one prompt of 16384 tokens in 256 slots takes 1954 and 1378.
+//
+// Few tiles: no more than SMs, of no more than six key tiles.  One prompt of 77, 200, 300,
+// 400, 500, 600 tokens (24 to 152 tiles) 7.3 7.9, 9.0 10.0, 10.8 11.8, 12.5 11.9, 12.9 13.4,
+// 14.6 14.7, of 650 and 800 17.0 15.4, 19.2 17.0; 64/8 heads of 128, 150 and 300 tokens
+// (80, 152 tiles) 9.2 9.8, 11.0 11.7; 8/8, 700 and 1100 (48, 72 tiles) 15.7 16.4, 21.0 19.6;
+// 32/8 of 64, 600 tokens 12.3 13.4.
 template <int DQ, int DV>
 cudaError_t launch_prompt_d(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                             const PromptParams& p, int num_sms, cudaStream_t stream) {
   if constexpr (DQ <= 128) {  // (three stages of 192 dims do not fit half an SM)
     const int64_t tokens = kTileM / (p.heads / p.kv_heads);
     const int64_t tiles = (p.total / tokens + std::min<int64_t>(p.batch, p.total)) * p.kv_heads;
-    if (p.total <= static_cast<int64_t>(kTileN) * p.batch || 5 * tiles <= 3 * num_sms)
+    const int64_t few_rows = DQ + DV <= 128 ? kTileN : std::max<int64_t>(tokens, 96);
+    if (p.total <= few_rows * p.batch || (tiles <= num_sms && p.total <= 6 * kTileN))
       return launch_prompt_t<DQ, DV, false>(tm_q, tm_k, tm_v, p, stream);
   }
   return launch_prompt_t<DQ, DV, true>(tm_q, tm_k, tm_v, p, stream);

@@ -553,6 +553,10 @@ size_t vpp_decode_attn_workspace_size(int32_t batch, int heads, int kv_heads,
  * 0 .. total_q or ends before it begins is left out and recorded as
  * VPP_ERR_INVALID.
  * A row whose scores are all -inf gets out = 0 and lse = -inf.
+ * The kernel's form follows total_q / batch, as the lengths are not known on
+ * the host: up to 96 to 128 rows a sequence it is the one for short prompts,
+ * which takes a long prompt 1.4 times as long.  A batch of fixed size with
+ * mostly empty sequences should therefore not have more than total_q / 128.
  * out [total_q][heads][head_dim_v] bf16, lse [heads][total_q] float32 (NULL
  * allowed).  No workspace; total_q == 0 is a no-op.
  */

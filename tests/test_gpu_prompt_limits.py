@@ -7,7 +7,7 @@ import torch
 
 from chunked_prefill_causal_gb300 import vpp
 from tests.serving_ref import HALF_BF16, attend, check_attention, randn
-from tests.test_gpu_prompt import starts
+from tests.test_gpu_prompt import LENS, SHAPES, check_sequences, starts, views
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -38,7 +38,7 @@ def test_rows_whose_scores_are_all_minus_infinity(H, Hkv, dq, dv, lens):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-@pytest.mark.parametrize("H,Hkv,dq,dv", [(32, 8, 128, 128), (24, 24, 192, 128), (12, 1, 192, 64), (5, 1, 64, 128), (8, 8, 64, 64), (26, 2, 128, 64)])
+@pytest.mark.parametrize("H,Hkv,dq,dv", [(32, 8, 128, 128), (20, 20, 192, 128), (12, 1, 192, 64), (5, 1, 64, 128), (8, 8, 64, 64), (26, 2, 128, 64)])
 def test_hostile_neighbours_of_long_sequences(H, Hkv, dq, dv, bad):
     """Sequences of many key tiles with partial last ones, several items a CTA, hostile values before, between and behind them."""
     lens = [40, 700, 1, 1500, 130, 300, 129, 385, 64, 1027, 5]
@@ -107,3 +107,18 @@ def test_the_cached_path_gives_the_same_attention():
     # each side: P to bf16, one rounding of the result to bf16 (see check_attention; 2^-14 holds its float32 terms at these sizes)
     tol = 2 * (HALF_BF16 * o.abs() + (HALF_BF16 + 2.0 ** -14) * absw)
     assert bool(((a - b).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("lens,rest", [(LENS + [0] * 4, 0), ([77, 20, 130, 1], 300), ([96] * 40, 0), ([97] * 40, 0), ([128] * 30, 0)])
+@pytest.mark.parametrize("H,Hkv,dq,dv", SHAPES + [(32, 8, 128, 128), (21, 7, 64, 128), (32, 8, 64, 64)])
+def test_both_forms(H, Hkv, dq, dv, lens, rest):
+    """Batches on both sides of the choice between one query tile a CTA and pairs of tiles."""
+    cu = starts(lens)
+    T = int(cu[-1]) + rest
+    x = randn((T, H * dq + Hkv * (dq + dv)), 13)
+    lse = torch.full((H, T), 7.0, device=DEV)
+    out = torch.full((T, H, dv), 7.0, dtype=torch.bfloat16, device=DEV)
+    vpp.vpp_prompt_attn(*views(x.to(DEV), H, Hkv, dq, dv), cu.to(DEV), out=out, lse=lse)
+    assert vpp.vpp_last_device_status() == 0
+    check_sequences(out, lse, *views(x, H, Hkv, dq, dv), cu, dq)
+    assert bool((out[int(cu[-1]):] == 7).all()) and bool((lse[:, int(cu[-1]):] == 7).all())

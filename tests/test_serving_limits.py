@@ -36,7 +36,7 @@ def test_workspace_holds_two_partials_a_column():
     def padded(n):
         return (n + 255) // 256 * 256
 
-    for heads, kv_heads, dq, dv, ctas in ((8, 2, 128, 128, 3), (64, 8, 128, 128, 3), (16, 16, 192, 128, 2), (5, 5, 64, 64, 3), (128, 128, 64, 128, 3)):
+    for heads, kv_heads, dq, dv, ctas in ((8, 2, 128, 128, 3), (64, 8, 128, 128, 3), (12, 12, 192, 128, 2), (5, 5, 64, 64, 3), (128, 128, 64, 128, 3)):
         c = max(columns(kv_heads, 2), columns(kv_heads, ctas))
         want = padded(c * 2 * heads * dv * 4) + padded(c * 2 * heads * 8) + padded(c * 16)
         assert vpp.decode_attn_workspace_size(3, heads, kv_heads, dq, dv) == want
