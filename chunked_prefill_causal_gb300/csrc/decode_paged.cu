@@ -12,7 +12,7 @@
 // 256 sequences of 1024 to 32768 tokens, 8 kv heads of 128, 16.6 GB in 2.26 to
 // 2.36 ms (7.05 to 7.35 TB/s by machine); 200 over an E4M3 cache 6.8 TB/s; one of
 // 131071 tokens, 537 MB, in 82 to 84 us (6.4 to 6.5 TB/s).  One of 1000 tokens takes
-// 6.2 us, the latency of two launches and of lengths -> block table -> page -> softmax
+// 6.3 us, the latency of two launches and of lengths -> block table -> page -> softmax
 // -> join.
 //
 // Work split.  The pages (64-token blocks) of all sequences, in order, form
@@ -76,10 +76,12 @@ constexpr float kLift = F8 ? 14.0f : 0.0f;
 template <bool F8>
 constexpr float kGrow = F8 ? 1.0f : 8.0f;
 
-// CTAs per SM: three where a stage is small and the registers of q and O leave room in
-// 128, else two.  (Two groups of heads over an E4M3 cache, 1.2 GB, two and three CTAs:
-// 64/64 dims 361 and 276 us, 128/64 259 and 232, 192/64 226 and 208; 128/128, which
-// spills, 228 and 343.  Over a bf16 cache 64/64 dims take 178 and 182 us.)
+// CTAs per SM: three where a stage is small and q and O take up to 80 registers of 128,
+// else two.  (Two groups of heads over an E4M3 cache, 1.2 GB, two and three CTAs: 64/64
+// dims 359 and 278 us, 64/128 277 and 264, 128/64 263 and 236, 192/64 229 and 207, the
+// last three with 44, 12 and 112 bytes a thread spilled; 128/128, whose q and O take 96,
+// 231 and 344.  Over a bf16 cache 64/64 dims take 178 and 182 us.)  192/128 dims with two
+// groups spill 36 (bf16) and 64 bytes (E4M3) at two CTAs too.
 constexpr int ctas_per_sm(int dq, int dv, bool f8, int ng) {
   return (ng == 1 || f8) && ng * (dq / 8 + dv / 4) <= 80 && (dq + dv) * (f8 ? 1 : 2) <= 256 ? 3 : 2;
 }

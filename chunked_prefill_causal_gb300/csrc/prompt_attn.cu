@@ -45,10 +45,10 @@
 //
 // Bound by the tensor core and the softmax that feeds it for long prompts: one of
 // 16384 tokens, 32/8 heads of 128, takes 1350 to 1380 us on a GB300, 1593 to 1629
-// TFLOP/s (83 to 85% of the cuBLAS rate; tensor pipe active 67% of the cycles, issue
-// slots 41%).  Bound by the chain of one item (first loads, first softmax, drain,
+// TFLOP/s (83 to 85% of the cuBLAS rate; tensor pipe active 68% of the cycles, issue
+// slots 42%).  Bound by the chain of one item (first loads, first softmax, drain,
 // output: 2.5 us beside its keys) for short ones: 24 prompts of 5 to 2500 tokens take
-// 106 us (984 TFLOP/s, tensor pipe 46%).  At 192 dims the ring holds a K tile, its V
+// 106 us (984 TFLOP/s, tensor pipe 47%).  At 192 dims the ring holds a K tile, its V
 // tile and the next K tile, no more, and each item starts by loading 96 KB of Q: three
 // prompts of 720 to 1026 tokens, 128 heads of their own keys, take 146 us, 2.2 times
 // their bytes' time.

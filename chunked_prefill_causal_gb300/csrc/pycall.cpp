@@ -2,7 +2,7 @@
 // operators, for vpp.py.  Their kernels take a few microseconds at decode sizes,
 // less than ctypes takes to convert thirty arguments, or Python's attribute calls to
 // read ten tensors (an append: 24.7 us of host time by ctypes, 6.8 us through attribute
-// calls from C, 2.9 us here; a decode call 23.5, 8.9 and 5.8 us); here the tensors'
+// calls from C, 2.8 us here; a decode call 23.5, 8.9 and 5.4 us); here the tensors'
 // own fields are read and the library's functions called by address.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

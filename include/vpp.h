@@ -424,7 +424,12 @@ size_t vpp_topk_chunk_attn_workspace_size(int64_t chunk_len, int32_t topk,
  * at least heads x d), so they may be parts of one fused projection
  * [total_q][heads dq + kv_heads dq + kv_heads dv]; out, lse and the caches
  * are contiguous.  heads / kv_heads is any whole number from 1 to 16; batch
- * and total_q are below 2^30.
+ * and total_q are below 2^30.  Outputs and workspaces overlap no input, except
+ * where a call says so.
+ * Attention: scores, maxima, denominators and sums are float32.  For the
+ * product with v a weight is rounded to bf16 (by 2^-8 of itself at most), over
+ * an E4M3 cache to f16 (by 2^-11 of itself, or 2^-39 of the row's largest
+ * weight where that is more); the result is rounded to bf16 once.
  */
 
 /*
